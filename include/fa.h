@@ -268,6 +268,66 @@ fa_status fa_backward_dropout_heads(const void* Q, const void* K, const void* V,
                                     size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * Attention with shaped scores and shared K/V heads (bf16, and f16 with the suffix _f16).
+ *   K, V, dK, dV: [B, Hkv, N, d] with Hkv dividing H; query head h uses K/V head
+ *     h / (H / Hkv), and dK, dV are the sums over the query heads that share it.
+ *   softcap: 0 for none, else c > 0 and the scores are capped: c * tanh(scale * q.k / c).
+ *     scale / c must lie in [2^-24, 2^12] (else FA_ERR_UNSUPPORTED).
+ *   slopes: NULL, or DEVICE memory, fp32 [H]: slopes[h] * |i - j| is subtracted from the
+ *     (capped) score of query i and key j. A constant: no gradient for it.
+ *   documents: NULL, or DEVICE memory, int32 [B, n_docs + 1], ascending offsets in [0, N]:
+ *     tokens of batch entry b in [documents[b][m], documents[b][m+1]) are its document m,
+ *     and query i sees key j only within one document. Tokens in front of the first offset
+ *     or behind the last are padding: they see nothing and nothing sees them (O = 0,
+ *     LSE = -inf, and zero dQ, dK, dV). Documents may be empty. Rows whose offsets do not
+ *     ascend or leave [0, N] give undefined results (offsets are clamped; no access leaves
+ *     the tensors).
+ *   prefix: NULL, or DEVICE memory, int32 [B, n_docs] ([B] without documents): the first
+ *     prefix[b][m] tokens of the document are seen by every query of it, whatever causal
+ *     and window_right say (window_left holds for them too). Negative counts as 0.
+ *   causal, window_left, window_right: as for fa_forward_masked.
+ * The tensors must be finite at padding positions as well (weights of 0 multiply them).
+ * n_docs is not read without documents. Workspace: fa_backward_workspace_size(B, H, N, d).
+ * Other arguments, errors and determinism as for fa_forward / fa_backward.
+ */
+fa_status fa_forward_scored(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                            int B, int H, int Hkv, int N, int d, float scale, int causal,
+                            int window_left, int window_right, float softcap,
+                            const float* slopes, const int32_t* documents, int n_docs,
+                            const int32_t* prefix, fa_stream_t stream);
+fa_status fa_backward_scored(const void* Q, const void* K, const void* V, const void* O,
+                             const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                             int B, int H, int Hkv, int N, int d, float scale, int causal,
+                             int window_left, int window_right, float softcap,
+                             const float* slopes, const int32_t* documents, int n_docs,
+                             const int32_t* prefix, void* workspace, size_t workspace_bytes,
+                             fa_stream_t stream);
+fa_status fa_forward_scored_f16(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                            int B, int H, int Hkv, int N, int d, float scale, int causal,
+                            int window_left, int window_right, float softcap,
+                            const float* slopes, const int32_t* documents, int n_docs,
+                            const int32_t* prefix, fa_stream_t stream);
+fa_status fa_backward_scored_f16(const void* Q, const void* K, const void* V, const void* O,
+                             const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                             int B, int H, int Hkv, int N, int d, float scale, int causal,
+                             int window_left, int window_right, float softcap,
+                             const float* slopes, const int32_t* documents, int n_docs,
+                             const int32_t* prefix, void* workspace, size_t workspace_bytes,
+                             fa_stream_t stream);
+
+/*
+ * Which keys and queries the masks of the scored calls join, for one batch entry. Host
+ * only; documents ([n_docs + 1]) and prefix ([n_docs]) are HOST memory here, or NULL.
+ *   what = 0: the keys [*lo, *hi) that query `index` sees; 1: the queries that see key
+ *   `index`; 2: the 128-key tiles that the forward walks for the 128 queries from `index`
+ *   on; 3: the 128-query tiles that the backward walks for the 128 keys from `index` on.
+ * An empty interval has *hi <= *lo.
+ */
+fa_status fa_score_span(const int32_t* documents, int n_docs, const int32_t* prefix, int N,
+                        int causal, int window_left, int window_right, int what, int index,
+                        int* lo, int* hi);
+
+/*
  * The drop probability the dropout calls apply for `p_drop`: floor(256 p_drop) / 256
  * (for example 0.1 gives 25/256 = 0.09765625). Returns -1 for a p_drop those calls
  * refuse (outside [0, 1), NaN, or in (0, 1/256)). Host only; no CUDA call.

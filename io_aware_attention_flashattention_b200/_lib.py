@@ -17,6 +17,11 @@ FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = ran
 # name -> (restype, argtypes), exactly the declarations of include/fa.h
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _u32, _u64 = ctypes.c_uint32, ctypes.c_uint64
+# B, H, Hkv, N, d, scale, causal, window_left, window_right, softcap, slopes, documents, n_docs,
+# prefix
+_SCORE = [_i, _i, _i, _i, _i, _f, _i, _i, _i, _f, _vp, _vp, _i, _vp]
+_SCORED_FWD = (_i, [_vp] * 5 + _SCORE + [_vp])
+_SCORED_BWD = (_i, [_vp] * 9 + _SCORE + [_vp, _sz, _vp])
 SIGNATURES = {
     "fa_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_backward_workspace_size": (_sz, [_i, _i, _i, _i]),
@@ -50,6 +55,11 @@ SIGNATURES = {
     "fa_forward_f32": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_backward_f32": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                              _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "fa_forward_scored": _SCORED_FWD,
+    "fa_backward_scored": _SCORED_BWD,
+    "fa_forward_scored_f16": _SCORED_FWD,
+    "fa_backward_scored_f16": _SCORED_BWD,
+    "fa_score_span": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp]),
     "fa_get_status": (_i, [_vp]),
     "fa_watchdog_selftest": (_i, [_i, _vp]),
     "fa_status_string": (ctypes.c_char_p, [_i]),

@@ -28,7 +28,8 @@ __all__ = [
     "fa_backward_preprocess", "fa_backward_main", "fa_backward_dq_convert",
     "fa_backward_noalloc", "fa_forward_f16", "fa_backward_f16", "fa_forward_masked",
     "fa_backward_masked", "fa_forward_dropout", "fa_backward_dropout", "fa_forward_f32",
-    "fa_backward_f32", "fa_get_status", "fa_watchdog_selftest", "fa_version", "fa_dropout_rate",
+    "fa_backward_f32", "fa_forward_scored", "fa_backward_scored", "fa_forward_scored_f16",
+    "fa_backward_scored_f16", "fa_get_status", "fa_watchdog_selftest", "fa_version", "fa_dropout_rate",
     "fa_launch_plan",
     "forward", "backward", "attention", "FlashAttentionFunction",
 ]
@@ -342,6 +343,96 @@ def fa_backward_f32(Q, K, V, O, dO, LSE, dQ, dK, dV, scale: float, causal: bool,
                                                    _stream(stream)))
 
 
+def _shared_heads(Q, K):
+    """(B, H, Hkv, N, d) of a call whose K/V heads are shared by groups of query heads."""
+    B, H, N, d = _shape(Q)
+    Hkv = _shape(K)[1]
+    if Hkv < 1 or H % Hkv:
+        raise ValueError(f"{H} query heads cannot share {Hkv} K/V heads evenly")
+    return B, H, Hkv, N, d
+
+
+def _device_array(name, t, dtype, shape):
+    """Device pointer of a contiguous CUDA tensor, or None for None."""
+    return None if t is None else _need(name, t, dtype, shape)
+
+
+def _score(B, H, softcap, slopes, documents, prefix):
+    """The C arguments softcap, slopes, documents, n_docs, prefix."""
+    n_docs = 1
+    if documents is not None:
+        if documents.dim() != 2 or documents.shape[1] < 2:
+            raise ValueError("documents must be a [B, documents + 1] tensor of offsets, got shape "
+                             f"{tuple(documents.shape)}")
+        n_docs = int(documents.shape[1]) - 1
+    if prefix is not None and prefix.dim() == 1 and documents is None:
+        prefix = prefix.unsqueeze(1)
+    return (0.0 if softcap is None else float(softcap),
+            _device_array("slopes", slopes, torch.float32, (H,)),
+            _device_array("documents", documents, torch.int32, (B, n_docs + 1)), n_docs,
+            _device_array("prefix", prefix, torch.int32, (B, n_docs)))
+
+
+def _forward_scored(name, dtype, Q, K, V, O, LSE, scale, causal, window, softcap, slopes,
+                    documents, prefix, stream):
+    B, H, Hkv, N, d = _shared_heads(Q, K)
+    args = [_need("Q", Q, dtype, (B, H, N, d)), _need("K", K, dtype, (B, Hkv, N, d)),
+            _need("V", V, dtype, (B, Hkv, N, d)), _need("O", O, dtype, (B, H, N, d)),
+            _need("LSE", LSE, torch.float32, (B, H, N))]
+    wl, wr = _window(window)
+    check(name, getattr(lib(), name)(
+        *args, B, H, Hkv, N, d, float(scale), int(bool(causal)), wl, wr,
+        *_score(B, H, softcap, slopes, documents, prefix), _stream(stream)))
+
+
+def _backward_scored(name, dtype, Q, K, V, O, dO, LSE, dQ, dK, dV, scale, causal, workspace,
+                     window, softcap, slopes, documents, prefix, stream):
+    B, H, Hkv, N, d = _shared_heads(Q, K)
+    sq, sk = (B, H, N, d), (B, Hkv, N, d)
+    ptrs = [_need("Q", Q, dtype, sq), _need("K", K, dtype, sk), _need("V", V, dtype, sk),
+            _need("O", O, dtype, sq), _need("dO", dO, dtype, sq),
+            _need("LSE", LSE, torch.float32, (B, H, N)),
+            _need("dQ", dQ, dtype, sq), _need("dK", dK, dtype, sk), _need("dV", dV, dtype, sk)]
+    ws, nbytes = _ws(workspace)
+    wl, wr = _window(window)
+    check(name, getattr(lib(), name)(
+        *ptrs, B, H, Hkv, N, d, float(scale), int(bool(causal)), wl, wr,
+        *_score(B, H, softcap, slopes, documents, prefix), ws, nbytes, _stream(stream)))
+
+
+@_on_one_device
+def fa_forward_scored(Q, K, V, O, LSE, scale: float, causal: bool, window=None, softcap=None,
+                      slopes=None, documents=None, prefix=None, stream=None) -> None:
+    """fa_forward with shaped scores (bf16): capped at ``softcap`` by a tanh, lowered by
+    ``slopes[h] * |i - j|``, within ``documents`` and with a ``prefix`` that every query
+    of the document sees; K and V may have fewer heads than Q."""
+    _forward_scored("fa_forward_scored", torch.bfloat16, Q, K, V, O, LSE, scale, causal, window,
+                    softcap, slopes, documents, prefix, stream)
+
+
+@_on_one_device
+def fa_forward_scored_f16(Q, K, V, O, LSE, scale: float, causal: bool, window=None, softcap=None,
+                          slopes=None, documents=None, prefix=None, stream=None) -> None:
+    _forward_scored("fa_forward_scored_f16", torch.float16, Q, K, V, O, LSE, scale, causal,
+                    window, softcap, slopes, documents, prefix, stream)
+
+
+@_on_one_device
+def fa_backward_scored(Q, K, V, O, dO, LSE, dQ, dK, dV, scale: float, causal: bool, workspace,
+                       window=None, softcap=None, slopes=None, documents=None, prefix=None,
+                       stream=None) -> None:
+    _backward_scored("fa_backward_scored", torch.bfloat16, Q, K, V, O, dO, LSE, dQ, dK, dV, scale,
+                     causal, workspace, window, softcap, slopes, documents, prefix, stream)
+
+
+@_on_one_device
+def fa_backward_scored_f16(Q, K, V, O, dO, LSE, dQ, dK, dV, scale: float, causal: bool,
+                           workspace, window=None, softcap=None, slopes=None, documents=None,
+                           prefix=None, stream=None) -> None:
+    _backward_scored("fa_backward_scored_f16", torch.float16, Q, K, V, O, dO, LSE, dQ, dK, dV,
+                     scale, causal, workspace, window, softcap, slopes, documents, prefix, stream)
+
+
 @_on_one_device
 def fa_get_status(stream=None) -> int:
     """Synchronises the stream; returns the library status code (0 = ok, 4 = a
@@ -365,16 +456,42 @@ def _masked(window, block_mask) -> bool:
     return window is not None or block_mask is not None
 
 
+def _scored(q, k, softcap, slopes, documents, prefix) -> bool:
+    return (softcap is not None or slopes is not None or documents is not None
+            or prefix is not None or (k.dim() == 4 and k.shape[1] != q.shape[1]))
+
+
+def _check_scored(q, block_mask, dropout) -> str:
+    """The suffix of the scored entry points for q's type; refuses what they do not take."""
+    if block_mask is not None or dropout is not None:
+        raise ValueError("block_mask and dropout do not combine with softcap, slopes, documents, "
+                         "prefix or shared K/V heads")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("softcap, slopes, documents, prefix and shared K/V heads are supported "
+                        "for bf16 and f16 inputs")
+    return "" if q.dtype == torch.bfloat16 else "_f16"
+
+
 def forward(q, k, v, causal: bool = False, scale=None, window=None, block_mask=None,
-            dropout=None):
+            dropout=None, softcap=None, slopes=None, documents=None, prefix=None):
     """(O, LSE) for bf16, f16 or fp32 q, k, v of shape [B, H, N, d] on the GPU.
     ``window`` / ``block_mask`` as for fa_forward_masked and ``dropout`` = (p, seed,
-    offset) as for fa_forward_dropout (bf16 only)."""
+    offset) as for fa_forward_dropout (bf16 only).
+
+    Shaped scores (bf16 and f16, see fa_forward_scored in include/fa.h): ``softcap`` caps
+    the scores by c * tanh(s / c); ``slopes`` (fp32 [H]) subtracts slopes[h] * |i - j|;
+    ``documents`` (int32 [B, M + 1]) holds the offsets of each row's documents, between
+    which nothing is seen; ``prefix`` (int32 [B, M], [B] without documents) the number of
+    first tokens that every query of the document sees. k and v may have fewer heads than
+    q (a divisor): query head h uses head h // (H // Hkv)."""
     B, H, N, d = _shape(q)
     scale = _default_scale(d, scale)
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    if dropout is not None:
+    if _scored(q, k, softcap, slopes, documents, prefix):
+        fn = fa_forward_scored_f16 if _check_scored(q, block_mask, dropout) else fa_forward_scored
+        fn(q, k, v, o, lse, scale, causal, window, softcap, slopes, documents, prefix)
+    elif dropout is not None:
         if q.dtype != torch.bfloat16:
             raise TypeError("dropout is supported for bf16 inputs")
         fa_forward_dropout(q, k, v, o, lse, scale, causal, dropout, window, block_mask)
@@ -400,13 +517,19 @@ def workspace_for(q) -> torch.Tensor:
 
 
 def backward(q, k, v, o, lse, do, causal: bool = False, scale=None, workspace=None,
-             window=None, block_mask=None, dropout=None):
-    """(dQ, dK, dV) of the loss <dO, O> (same masks and dropout as the forward)."""
+             window=None, block_mask=None, dropout=None, softcap=None, slopes=None,
+             documents=None, prefix=None):
+    """(dQ, dK, dV) of the loss <dO, O> (same masks, dropout and scores as the forward)."""
     B, H, N, d = _shape(q)
     scale = _default_scale(d, scale)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ws = workspace_for(q) if workspace is None else workspace
-    if dropout is not None:
+    if _scored(q, k, softcap, slopes, documents, prefix):
+        fn = (fa_backward_scored_f16 if _check_scored(q, block_mask, dropout)
+              else fa_backward_scored)
+        fn(q, k, v, o, do, lse, dq, dk, dv, scale, causal, ws, window, softcap, slopes,
+           documents, prefix)
+    elif dropout is not None:
         if q.dtype != torch.bfloat16:
             raise TypeError("dropout is supported for bf16 inputs")
         fa_backward_dropout(q, k, v, o, do, lse, dq, dk, dv, scale, causal, ws, dropout, window,
@@ -432,25 +555,32 @@ class FlashAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, causal: bool = False, scale=None, window=None, block_mask=None,
-                dropout=None):
+                dropout=None, softcap=None, slopes=None, documents=None, prefix=None):
+        if slopes is not None and slopes.requires_grad:
+            raise ValueError("slopes are constants: they have no gradient")
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-        o, lse = forward(q, k, v, causal, scale, window, block_mask, dropout)
-        ctx.save_for_backward(q, k, v, o, lse)
+        o, lse = forward(q, k, v, causal, scale, window, block_mask, dropout, softcap, slopes,
+                         documents, prefix)
+        ctx.save_for_backward(q, k, v, o, lse, slopes, documents, prefix)
         ctx.causal, ctx.scale, ctx.window, ctx.block_mask = causal, scale, window, block_mask
         ctx.dropout = dropout  # the backward regenerates the same keep mask
+        ctx.softcap = softcap
         return o
 
     @staticmethod
     def backward(ctx, do):
-        q, k, v, o, lse = ctx.saved_tensors
+        q, k, v, o, lse, slopes, documents, prefix = ctx.saved_tensors
         dq, dk, dv = backward(q, k, v, o, lse, do.contiguous(), ctx.causal, ctx.scale,
                               window=ctx.window, block_mask=ctx.block_mask,
-                              dropout=ctx.dropout)
-        return dq, dk, dv, None, None, None, None, None
+                              dropout=ctx.dropout, softcap=ctx.softcap, slopes=slopes,
+                              documents=documents, prefix=prefix)
+        return (dq, dk, dv) + (None,) * (len(ctx.needs_input_grad) - 3)
 
 
 def attention(q, k, v, causal: bool = False, scale=None, window=None, block_mask=None,
-              dropout=None):
+              dropout=None, softcap=None, slopes=None, documents=None, prefix=None):
     """Differentiable attention; ``dropout`` = (p, seed, offset): pass a new offset (or
-    seed) per call to draw a new mask."""
-    return FlashAttentionFunction.apply(q, k, v, causal, scale, window, block_mask, dropout)
+    seed) per call to draw a new mask. ``softcap``, ``slopes``, ``documents`` and
+    ``prefix`` as for ``forward``; slopes are constants (no gradient)."""
+    return FlashAttentionFunction.apply(q, k, v, causal, scale, window, block_mask, dropout,
+                                        softcap, slopes, documents, prefix)

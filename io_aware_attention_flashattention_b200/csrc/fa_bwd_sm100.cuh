@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "fa_ptx.cuh"
+#include "fa_score.cuh"
 
 namespace fa {
 namespace bwd {
@@ -116,6 +117,7 @@ struct Params {
   int wr;                 // keys j <= i + wr are kept; < 0: no right bound (causal: 0)
   const uint8_t* blocks;  // [n_kt x n_kt] block mask (nonzero = kept), or null
   DropoutParams drop;     // used by the kDropout instances only
+  ScoreParams score;      // used by the kScore instances only (there BH counts K/V heads)
   unsigned long long timeout_ns;
   // Split key tiles (no block mask): the last n_split tiles (head-major) have their
   // query steps cut in two segments, [0, a) and [a, steps) with a = steps * split_num /
@@ -289,12 +291,15 @@ __global__ void __launch_bounds__(256)
 // kM: test each query against the key's visible range [q_lo, q_hi): query qh0 + x is
 // visible iff qoff + x < q_span (unsigned). ctr_head: the dropout counter's head word
 // (the call's head_base + the flattened head).
-template <Elt E, bool kDropout, bool kM>
+// kScore: S^T is first brought to the shaped score (c turns it to log2 units); with a cap
+// dS takes the factor 1 - tanh^2, the derivative of the capped score by scale * q.k.
+template <Elt E, bool kDropout, bool kM, int kScore = 0>
 __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const float4* Lv,
                                           const float4* Dv4, float c, int key, int qh0,
                                           uint32_t ctr_head,
                                           const DropoutParams& drop, int lane, int qoff,
-                                          unsigned q_span, uint8_t* ds_row, int krow) {
+                                          unsigned q_span, uint8_t* ds_row, int krow,
+                                          const ScoreParams& score, float slope_neg) {
   uint32_t sv[2][16], dv[2][16];
   tmem_ld16(tm_s, sv[0]);
   tmem_ld16(tm_dp, dv[0]);
@@ -306,6 +311,15 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
       tmem_ld16(tm_s + 16 * (cc + 1), sv[cur ^ 1]);
       tmem_ld16(tm_dp + 16 * (cc + 1), dv[cur ^ 1]);
     }
+    // tanh of the chunk's scores, kept apart from the bias for the derivative
+    [[maybe_unused]] uint32_t th[(kScore & kScoreCap) ? 16 : 1];
+    if constexpr ((kScore & kScoreCap) != 0) {
+      tanh_scores(sv[cur], score);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) th[k] = sv[cur][k];
+    }
+    if constexpr ((kScore & kScoreBias) != 0)
+      bias_scores(sv[cur], qh0 + 16 * cc - key, slope_neg);
     // Dropout bytes of this key for the chunk's 16 queries: byte e of zq[v] is
     // query 16cc + 4v + e of the half. One block covers 4 queries x 4 keys, and
     // the lanes of keys 4g..4g+3 share its counter: lane u draws the block of the
@@ -351,6 +365,10 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
         } else {
           pv[e] = pe;
           dsv[e] = pe * (__uint_as_float(dv[cur][k]) - Ds[e]);
+          if constexpr ((kScore & kScoreCap) != 0) {
+            const float y = __uint_as_float(th[k]);
+            dsv[e] = fmaf(-y * y, dsv[e], dsv[e]);
+          }
         }
       }
       pk[2 * v] = pack2<E>(pv[0], pv[1]);
@@ -371,7 +389,7 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
 
 // ------------------------------------------------------------------ main kernel
 
-template <int D, Elt E, bool kMasked, bool kDropout = false>
+template <int D, Elt E, bool kMasked, bool kDropout = false, int kScore = 0>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -416,8 +434,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_q = (p.N + BM - 1) / BM;
   // query tiles [i_lo, i_hi) hold every query that may see a key of this tile
   const int k1 = min(k0 + BN, p.N) - 1;
-  const int i_lo_tile = (wr < 0) ? 0 : max(0, k0 - wr) / BM;
-  const int i_hi_tile = (wl < 0) ? n_q : min(n_q, (k1 + wl) / BM + 1);
+  int i_lo_tile = (wr < 0) ? 0 : max(0, k0 - wr) / BM;
+  int i_hi_tile = (wl < 0) ? n_q : min(n_q, (k1 + wl) / BM + 1);
+  // kScore: bh is a K/V head; the CTA walks the query tiles of each head that shares it,
+  // one head after the other. docs, prefix: this batch entry's own.
+  const int n_share = kScore ? p.score.group : 1;
+  const int b_of = kScore ? bh / (p.score.H / p.score.group) : 0;
+  const int* const docs =
+      (kScore && p.score.docs) ? p.score.docs + static_cast<size_t>(b_of) * (p.score.n_docs + 1)
+                               : nullptr;
+  const int* const prefix =
+      (kScore && p.score.prefix) ? p.score.prefix + static_cast<size_t>(b_of) * p.score.n_docs
+                                 : nullptr;
+  if constexpr (kScore != 0) {
+    pdl_wait();  // the offsets may come from the grid before
+    const Span s = query_tiles_of_keys(docs, prefix, p.score.n_docs, p.N, wl, wr, k0);
+    i_lo_tile = s.lo;
+    i_hi_tile = s.hi;
+  }
   // a split tile's segment walks a sub-range of the query tiles (no block mask then)
   int i_lo = i_lo_tile, i_hi = i_hi_tile;
   if (seg >= 0) {
@@ -479,6 +513,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     nsteps = 0;
     for (int i = i_lo; i < i_hi; ++i) nsteps += member(i) ? 1 : 0;
   }
+  if constexpr (kScore != 0) nsteps *= n_share;
+  // the next step's query tile i, and the head whose queries these are (bhq)
+  auto advance = [&](int& i, int& bhq) {
+    if constexpr (kScore != 0) {
+      if (++i >= i_hi) {
+        i = i_lo;
+        ++bhq;
+      }
+    } else {
+      do ++i; while (!member(i));
+    }
+  };
+  const int bhq0 = kScore ? bh * n_share : bh;
 
   // ring of half tiles: seq = 4*step + 2*h + w, w = 0 for dO (rows 64h.. of query
   // tile i), w = 1 for Q (with L2 and D of those 64 queries)
@@ -505,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int issued = 0;
     bool ok = true;
-    int i = i_lo - 1;
+    int i = i_lo - 1, bhq = bhq0;
     for (int s = 0; s < nsteps && ok; ++s) {
-      do ++i; while (!member(i));
+      advance(i, bhq);
       for (int hw = 0; hw < 4 && ok; ++hw) {
         const int h = hw >> 1, w = hw & 1;
         const int seq = seq_of(s, h, w);
@@ -525,14 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w == 1) {
           mbar_arrive_expect_tx_e(full, C::kHalfBytes + 2 * C::kVecBytes);
           const uint32_t vec = base + C::kVecOff + slot * 2 * C::kVecBytes;
-          const size_t off = static_cast<size_t>(bh) * p.Npad + static_cast<size_t>(row0);
+          const size_t off = static_cast<size_t>(bhq) * p.Npad + static_cast<size_t>(row0);
           bulk_load_e(vec, p.L2 + off, C::kVecBytes, full);
           bulk_load_e(vec + C::kVecBytes, p.Dv + off, C::kVecBytes, full);
         } else {
           mbar_arrive_expect_tx_e(full, C::kHalfBytes);
         }
         for (int c = 0; c < C::kChunks; ++c)
-          tma_load_3d_e(dst + c * C::kHalfChunkBytes, w ? &tmQ : &tmdO, full, c * 64, row0, bh);
+          tma_load_3d_e(dst + c * C::kHalfChunkBytes, w ? &tmQ : &tmdO, full, c * 64, row0, bhq);
         FA_TRACE_POINT(32, seq, 0);
         issued = seq + 1;
       }
@@ -621,14 +668,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool ragged_keys = k0 + BN > p.N;
     const int dq_bar = (D == 128) ? C::kBarDQFull + h : C::kBarDQFull;
     // queries that see this key row: [q_lo, q_hi) (empty for a padding key)
-    const int q_lo = (wr < 0) ? 0 : key - wr;
-    const int q_hi = (key >= p.N) ? q_lo : ((wl < 0) ? p.Npad + BM : key + wl + 1);
+    int q_lo = (wr < 0) ? 0 : key - wr;
+    int q_hi = (key >= p.N) ? q_lo : ((wl < 0) ? p.Npad + BM : key + wl + 1);
+    [[maybe_unused]] int full_lo = 0, full_hi = 0;  // kScore: queries that see all 32 keys
+    if constexpr (kScore != 0) {
+      const Span qs = queries_of_key(docs, prefix, p.score.n_docs, p.N, wl, wr, key);
+      q_lo = qs.lo;
+      // an interval up to N reaches over the padding rows too: their L2 = +inf gives P = 0
+      q_hi = (qs.hi == p.N && qs.hi > qs.lo) ? p.Npad : qs.hi;
+      full_lo = __reduce_max_sync(0xffffffffu, q_lo);
+      full_hi = __reduce_min_sync(0xffffffffu, q_hi);
+    }
     const unsigned q_span = static_cast<unsigned>(q_hi - q_lo);
     const uint32_t ctr_head = p.drop.head_base + static_cast<uint32_t>(bh);  // dropout
     bool ok = true;
-    int i = i_lo - 1;
+    int i = i_lo - 1, bhq = bhq0;
     for (int s = 0; s < nsteps && ok; ++s) {
-      do ++i; while (!member(i));
+      advance(i, bhq);
       const int qh0 = i * BM + 64 * h;  // first query of this half
       // The two barriers that completed long ago are observed first, so that the work
       // starts as soon as S^T and dP^T are in TMEM: the dQ MMA of the last step has
@@ -650,17 +706,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4* Dv4 = Lv + 64 / 4;
       // masking is needed only where the half crosses an edge of some key's visible
       // queries (the causal diagonal, a window edge) and on a ragged key tile
-      const bool mask = ragged_keys || (wr >= 0 && k0 + BN - 1 - wr > qh0) ||
-                        (wl >= 0 && k0 + wl < qh0 + 63);
+      const bool mask = kScore ? (qh0 < full_lo || qh0 + 64 > full_hi)
+                               : (ragged_keys || (wr >= 0 && k0 + BN - 1 - wr > qh0) ||
+                                  (wl >= 0 && k0 + wl < qh0 + 63));
+      float slope_neg = 0.0f;
+      if constexpr ((kScore & kScoreBias) != 0)
+        slope_neg = -p.score.slopes[bhq % p.score.H] * p.score.slope_mul;
       const int qoff = qh0 - q_lo;  // query qh0 + x is visible iff qoff + x < q_span (unsigned)
       // The element loop in two compiled forms: with the mask tests only on steps
       // that cross a mask edge, none on all the others.
       if (mask)
-        p_ds_half<E, kDropout, true>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
-                                     qoff, q_span, ds_row, krow);
+        p_ds_half<E, kDropout, true, kScore>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop,
+                                             lane, qoff, q_span, ds_row, krow, p.score, slope_neg);
       else
-        p_ds_half<E, kDropout, false>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
-                                      qoff, q_span, ds_row, krow);
+        p_ds_half<E, kDropout, false, kScore>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop,
+                                              lane, qoff, q_span, ds_row, krow, p.score,
+                                              slope_neg);
       tmem_wait_st();
       fence_proxy_async_smem();
       tc_fence_before();
@@ -764,9 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const int row = wq * 32 + lane;  // TMEM lane: head-dim element (D = 128) or query (D = 64)
     bool ok = true;
-    int i = i_lo - 1;
+    int i = i_lo - 1, bhq = bhq0;
     for (int s = 0; s < nsteps && ok; ++s) {
-      do ++i; while (!member(i));
+      advance(i, bhq);
       const int q0 = i * BM;
       if constexpr (D == 128) {
         for (int h = 0; h < 2 && ok; ++h) {
@@ -784,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (warp == kWarpDq) FA_TRACE_POINT(22, s, h);
           // element `row` of the head dimension for 64 queries: a warp covers 32
           // consecutive elements of one query row (128 contiguous bytes) per add
-          float* dst = p.dQacc + (static_cast<size_t>(bh) * p.N + q0 + 64 * h) * D + row;
+          float* dst = p.dQacc + (static_cast<size_t>(bhq) * p.N + q0 + 64 * h) * D + row;
           const int nq = min(64, p.N - (q0 + 64 * h));
 #pragma unroll
           for (int qq = 0; qq < 64; ++qq)
@@ -804,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(C::kBarDQEmpty));
         const int q = q0 + row;
         if (q < p.N) {
-          float* dst = p.dQacc + (static_cast<size_t>(bh) * p.N + q) * D;
+          float* dst = p.dQacc + (static_cast<size_t>(bhq) * p.N + q) * D;
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             red_add_v4(dst + 4 * k, __uint_as_float(v[k / 8][(4 * k) % 32]),
@@ -1122,10 +1183,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qoff = qh0 - q_lo;
         if (mask)
           p_ds_half<E, kDropout, true>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
-                                       qoff, q_span, ds_row, krow);
+                                       qoff, q_span, ds_row, krow, p.score, 0.0f);
         else
           p_ds_half<E, kDropout, false>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
-                                        qoff, q_span, ds_row, krow);
+                                        qoff, q_span, ds_row, krow, p.score, 0.0f);
         tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();

@@ -40,6 +40,7 @@
 #pragma once
 
 #include "fa_ptx.cuh"
+#include "fa_score.cuh"
 
 namespace fa {
 namespace fwd {
@@ -123,7 +124,17 @@ struct Params {
   const uint8_t* blocks;  // [n_kt x n_kt] block mask (nonzero = kept), or null
   int n_kt;               // ceil(N / 128)
   DropoutParams drop;     // used by the kDropout instances only
+  ScoreParams score;      // used by the kScore instances only
   unsigned long long timeout_ns;
+};
+
+// What a softmax thread of a kScore instance knows of its row: the keys [k_lo, k_hi) that
+// the row sees, those that every row of its warp sees, and its head's slope (negated, in
+// units of the scores before scale_log2).
+struct RowScore {
+  int k_lo, k_hi;
+  int full_lo, full_hi;
+  float slope_neg;
 };
 
 // S = Q_t K_j^T: M = 128 query rows, N = 128 keys, K = D; both operands K-major.
@@ -172,8 +183,10 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
 // - m_ref), their sum l and, rounded to 16 bits, P_t into the swizzled shared tile (with
 // dropout applied after the sum); then PFull. n counts this tile's S and PV products
 // before this one (their barrier phases); first: no PV_t of the item yet. Returns false
-// if a bounded wait gave up.
-template <int D, Elt E, bool kDropout>
+// if a bounded wait gave up. kScore: S is first brought to the shaped score, in units that
+// scale_log2 turns to log2 (see ScoreParams), chunk by chunk as it leaves TMEM; the row's
+// visible keys come from rs instead of wl and wr.
+template <int D, Elt E, bool kDropout, int kScore = 0>
 __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog& wd,
                                                  uint32_t tm_s, uint32_t tm_o, uint8_t* p_row,
                                                  uint32_t bar_sfree, uint32_t bar_pvdone,
@@ -181,13 +194,13 @@ __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog
                                                  int r0, int row, int row_in_tile, int wl,
                                                  int wr, uint32_t ctr_head, int lane,
                                                  int wq, int t, float& m_ref, float& l,
-                                                 float& lr) {
+                                                 float& lr, const RowScore& rs) {
   using C = Cfg<D>;
   const float c = p.scale_log2;
   const int r1 = r0 + BM - 1;
   // visible keys of this row: [k_lo, k_hi)
-  const int k_lo = (wl < 0) ? 0 : row - wl;
-  const int k_hi = (wr < 0) ? p.N : min(p.N, row + wr + 1);
+  const int k_lo = kScore ? rs.k_lo : ((wl < 0) ? 0 : row - wl);
+  const int k_hi = kScore ? rs.k_hi : ((wr < 0) ? p.N : min(p.N, row + wr + 1));
   tc_fence_after();
   uint32_t s[4][32];
 #pragma unroll
@@ -199,9 +212,18 @@ __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog
   if (lane == 0) mbar_arrive(bar_sfree);
   if (wq == 0) FA_TRACE_POINT(52, n, t);
   const int kv0 = kt * BN;
+  if constexpr ((kScore & kScoreCap) != 0) {
+#pragma unroll
+    for (int cc = 0; cc < 4; ++cc) tanh_scores(s[cc], p.score);
+  }
+  if constexpr ((kScore & kScoreBias) != 0) {
+#pragma unroll
+    for (int cc = 0; cc < 4; ++cc) bias_scores(s[cc], kv0 + 32 * cc - row, rs.slope_neg);
+  }
   // masking only where the tile crosses an edge of some row's visible range
-  const bool need_mask = (kv0 + BN > p.N) || (wr >= 0 && kv0 + BN - 1 > r0 + wr) ||
-                         (wl >= 0 && kv0 < r1 - wl);
+  const bool need_mask = kScore ? (kv0 < rs.full_lo || kv0 + BN > rs.full_hi)
+                                : ((kv0 + BN > p.N) || (wr >= 0 && kv0 + BN - 1 > r0 + wr) ||
+                                   (wl >= 0 && kv0 < r1 - wl));
   if (need_mask) {
     // key kv0 + k is visible iff 0 <= kv0 + k - k_lo < k_hi - k_lo
     const int off = kv0 - k_lo;
@@ -327,7 +349,7 @@ __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog
   return true;
 }
 
-template <int D, Elt E, bool kMasked, bool kDropout = false>
+template <int D, Elt E, bool kMasked, bool kDropout = false, int kScore = 0>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const Params p) {
@@ -371,17 +393,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int q0 = qt0 * BM;
   const int n_kt = p.n_kt;
+  // kScore: this batch entry's documents and prefixes, and the K/V head
+  const int b_of = kScore ? bh / p.score.H : 0;
+  const int* const docs =
+      (kScore && p.score.docs) ? p.score.docs + static_cast<size_t>(b_of) * (p.score.n_docs + 1)
+                               : nullptr;
+  const int* const prefix =
+      (kScore && p.score.prefix) ? p.score.prefix + static_cast<size_t>(b_of) * p.score.n_docs
+                                 : nullptr;
+  const int bh_kv = kScore ? bh / p.score.group : bh;
+  if constexpr (kScore != 0) pdl_wait();  // the offsets may come from the grid before
   // key tiles [lo[t], hi[t]) hold every key a row of query tile t may see
   int lo[2], hi[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int r0 = q0 + t * BM, r1 = min(r0 + BM, p.N) - 1;
-    lo[t] = (wl < 0) ? 0 : max(0, r0 - wl) / BN;
-    hi[t] = (wr < 0) ? n_kt : min(n_kt, (r1 + wr) / BN + 1);
+    if constexpr (kScore != 0) {
+      const Span s = key_tiles_of_rows(docs, prefix, p.score.n_docs, p.N, wl, wr, r0);
+      lo[t] = s.lo;
+      hi[t] = s.hi;
+    } else {
+      lo[t] = (wl < 0) ? 0 : max(0, r0 - wl) / BN;
+      hi[t] = (wr < 0) ? n_kt : min(n_kt, (r1 + wr) / BN + 1);
+    }
     if (r0 >= p.N || (t == 1 && !own1)) lo[t] = hi[t] = 0;
   }
-  // The CTA's key tiles: the union of both ranges (contiguous: lo[1] <= hi[0]).
-  const int kt_lo = (hi[0] > lo[0]) ? lo[0] : lo[1];
+  // The CTA's key tiles: the union of both ranges (contiguous: lo[1] <= hi[0]; kScore: as
+  // long as the offsets ascend, and the walk below passes over a gap in any case).
+  const int kt_lo = (hi[0] > lo[0]) ? ((kScore && hi[1] > lo[1]) ? min(lo[0], lo[1]) : lo[0])
+                                    : lo[1];
   const int kt_hi = max(hi[0], hi[1]);
 
   // Block mask rows of the two query tiles as bits in shared memory: warp w builds
@@ -490,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dst = is_k ? k_smem(j) : v_smem(j);
       mbar_arrive_expect_tx_e(bar(bfull + slot), C::kTileBytes);
       for (int c = 0; c < C::kChunks; ++c)
-        tma_load_3d_e(dst + c * C::kChunkBytes, map, bar(bfull + slot), c * 64, kt * BN, bh);
+        tma_load_3d_e(dst + c * C::kChunkBytes, map, bar(bfull + slot), c * 64, kt * BN, bh_kv);
       issued = j + 1;
     }
     // Every issued copy must land before the CTA may exit.
@@ -603,6 +643,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // the dropout counter's head word: the call's head_base + the flattened head
     const uint32_t ctr_head = p.drop.head_base + static_cast<uint32_t>(bh);
+    RowScore rs{};
+    if constexpr (kScore != 0) {
+      const Span ks = keys_of_query(docs, prefix, p.score.n_docs, p.N, wl, wr, row);
+      rs.k_lo = ks.lo;
+      rs.k_hi = ks.hi;
+      // rows behind N are not written: they ask for no element tests
+      rs.full_lo = __reduce_max_sync(0xffffffffu, row < p.N ? ks.lo : 0);
+      rs.full_hi = __reduce_min_sync(0xffffffffu, row < p.N ? ks.hi : p.N);
+      if constexpr ((kScore & kScoreBias) != 0)
+        rs.slope_neg = -p.score.slopes[bh % p.score.H] * p.score.slope_mul;
+    }
     bool ok = t_nk > 0;
     int kt = t_lo - 1;
     for (int j = 0; j < t_nk && ok; ++j) {
@@ -612,10 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (wq == 0) FA_TRACE_POINT(51, j, t);
       if (j == 0 && t == 0 && threadIdx.x == 0) FA_TRACE_CTA(2);
       if (!ok) break;
-      if (!softmax_key_tile<D, E, kDropout>(p, wd, tm_s, tm_o, p_row, bar(C::kBarSFree + t),
-                                            bar(C::kBarPVDone + t), bar(C::kBarPFull + t), j,
-                                            j == 0, kt, r0, row, row_in_tile, wl,
-                                            wr, ctr_head, lane, wq, t, m_ref, l, lr)) {
+      if (!softmax_key_tile<D, E, kDropout, kScore>(
+              p, wd, tm_s, tm_o, p_row, bar(C::kBarSFree + t), bar(C::kBarPVDone + t),
+              bar(C::kBarPFull + t), j, j == 0, kt, r0, row, row_in_tile, wl, wr, ctr_head, lane,
+              wq, t, m_ref, l, lr, rs)) {
         ok = false;
         break;
       }
@@ -1000,7 +1051,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!softmax_key_tile<D, E, kDropout>(p, wd, tm_s, tm_o, p_row, bar(C::kBarSFree + t),
                                               bar(C::kBarPVDone + t), bar(C::kBarPFull + t),
                                               n, j == 0, kt, r0, row, row_in_tile,
-                                              wl, wr, ctr_head, lane, wq, t, m_ref, l, lr)) {
+                                              wl, wr, ctr_head, lane, wq, t, m_ref, l, lr,
+                                              RowScore{})) {
           ok = false;
           break;
         }

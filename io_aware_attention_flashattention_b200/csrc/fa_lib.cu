@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "fa_ptx.cuh"
+#include "fa_score.cuh"
 #include "fa_fwd_sm100.cuh"
 #include "fa_bwd_sm100.cuh"
 #include "fa_simt_f32.cuh"
@@ -153,6 +154,12 @@ cudaError_t set_smem(Kern k, size_t bytes) {
                               static_cast<int>(bytes));
 }
 
+template <int D, Elt E, int kScore>
+cudaError_t set_smem_score() {
+  cudaError_t e = set_smem(fwd::fa_fwd_kernel<D, E, true, false, kScore>, fwd::Cfg<D>::kSmemBytes);
+  return e ? e : set_smem(bwd::fa_bwd_kernel<D, E, true, false, kScore>, bwd::Cfg<D>::kSmemBytes);
+}
+
 template <int D, Elt E>
 cudaError_t set_smem_d() {
   constexpr size_t S = fwd::Cfg<D>::kSmemBytes;
@@ -164,6 +171,10 @@ cudaError_t set_smem_d() {
   e = e ? e : set_smem(bwd::fa_bwd_kernel<D, E, true>, bwd::Cfg<D>::kSmemBytes);
   e = e ? e : set_smem(bwd::fa_bwd_persistent_kernel<D, E, false, false>, bwd::Cfg<D>::kSmemBytes);
   e = e ? e : set_smem(bwd::fa_bwd_persistent_kernel<D, E, true, false>, bwd::Cfg<D>::kSmemBytes);
+  e = e ? e : set_smem_score<D, E, kScoreOn>();
+  e = e ? e : set_smem_score<D, E, kScoreOn | kScoreCap>();
+  e = e ? e : set_smem_score<D, E, kScoreOn | kScoreBias>();
+  e = e ? e : set_smem_score<D, E, kScoreOn | kScoreCap | kScoreBias>();
   return e;
 }
 
@@ -416,7 +427,9 @@ double fwd_makespan_persistent(int BH, int n_qt, int singles, int sms, bool weig
   return *std::max_element(load.begin(), load.end());
 }
 
-FwdSplit fwd_split(int BH, int N, int d, int wl, int wr, bool block_mask, int sms) {
+// may_persist = false: one CTA per item in any case (the shaped-score kernels).
+FwdSplit fwd_split(int BH, int N, int d, int wl, int wr, bool block_mask, int sms,
+                   bool may_persist = true) {
   const int n_qt = (N + fwd::BM - 1) / fwd::BM;
   const int n_kt = (N + fwd::BN - 1) / fwd::BN;
   const int min_singles = n_qt % 2;
@@ -430,8 +443,8 @@ FwdSplit fwd_split(int BH, int N, int d, int wl, int wr, bool block_mask, int sm
   if (candidates * BH * n_qt > (1ll << 22)) return plain;
   static std::mutex mu;
   // at most 1024 shapes
-  static std::map<std::tuple<int, int, int, int, int, bool, int>, FwdSplit> cache;
-  const auto key = std::make_tuple(BH, N, d, wl, wr, block_mask, sms);
+  static std::map<std::tuple<int, int, int, int, int, bool, int, bool>, FwdSplit> cache;
+  const auto key = std::make_tuple(BH, N, d, wl, wr, block_mask, sms, may_persist);
   {
     std::lock_guard<std::mutex> lock(mu);
     auto it = cache.find(key);
@@ -469,7 +482,7 @@ FwdSplit fwd_split(int BH, int N, int d, int wl, int wr, bool block_mask, int sm
   // issue loop
   const long long pers_items = static_cast<long long>(BH) * ((n_qt - sg_pers) / 2 + sg_pers);
   const bool persistent =
-      !block_mask && pers_items > sms &&
+      may_persist && !block_mask && pers_items > sms &&
       fwd_makespan_grid(BH, n_qt, sg_grid, sms, key_tiles, kFwdGridCtaOverhead, wm_grid) >
           kFwdPersistMargin * kFwdPersistPenalty * t_pers;
   FwdSplit best = persistent ? FwdSplit{(n_qt - sg_pers) / 2, sg_pers, wm ? 1 : 0, 1}
@@ -875,6 +888,194 @@ fa_status backward_impl(const void* Q, const void* K, const void* V, const void*
   return dq_convert_impl<E>(dQ, B, H, N, d, scale, workspace, workspace_bytes, stream, split_ok);
 }
 
+// ---------------------------------------------------------------- shaped scores
+
+// softcap 0: none. The polynomial of tanh (see kTanhQ) takes the powers of a = scale / cap
+// into its coefficients, up to a^9, which must stay normal numbers: for a >= 2^-13 it is
+// used up to |x| = 0.7; below, its Taylor form of three terms up to |x| = 0.05, where the
+// next term is 8e-10 of the result. 1 - 2 / (1 + e^2x) takes over above, where its absolute
+// error of about 2e-7 is small next to x. So a is held to [2^-24, 2^12].
+fa_status make_score(int B, int H, int Hkv, float scale, float softcap, const float* slopes,
+                     const int32_t* documents, int n_docs, const int32_t* prefix,
+                     ScoreParams* s) {
+  if (Hkv < 1 || H < 1 || B < 1) return FA_ERR_INVALID_ARG;
+  if (H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(softcap) && softcap >= 0.0f)) return FA_ERR_INVALID_ARG;
+  if (documents != nullptr && n_docs < 1) return FA_ERR_INVALID_ARG;
+  if (n_docs > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(slopes), static_cast<const void*>(documents),
+                        static_cast<const void*>(prefix)})
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  *s = ScoreParams{};
+  s->slopes = slopes;
+  s->docs = documents;
+  s->prefix = prefix;
+  s->n_docs = documents != nullptr ? n_docs : 1;
+  s->H = H;
+  s->group = H / Hkv;
+  if (softcap > 0.0f) {
+    const double a = static_cast<double>(scale) / softcap;
+    if (!(a >= 1.0 / (1 << 24) && a <= 4096.0)) return FA_ERR_UNSUPPORTED;
+    const bool full = a >= 1.0 / 8192;
+    const double taylor[5] = {1.0, -1.0 / 3, 2.0 / 15, 0.0, 0.0};
+    double pw = a;
+    for (int k = 0; k < 5; ++k, pw *= a * a)
+      s->q[k] = static_cast<float>((full ? kTanhQ[k] : taylor[k]) * pw);
+    const double lim = (full ? static_cast<double>(kTanhLimit) : 0.05) / a;
+    s->lim2 = static_cast<float>(lim * lim);
+    s->cap_in2 = static_cast<float>(2.0 * 1.4426950408889634 * a);
+  }
+  s->slope_mul = softcap > 0.0f ? 1.0f / softcap : 1.0f / scale;
+  return FA_OK;
+}
+
+int score_bits(float softcap, const float* slopes) {
+  return kScoreOn | (softcap > 0.0f ? kScoreCap : 0) | (slopes != nullptr ? kScoreBias : 0);
+}
+
+// Scores before this factor to log2 units (see fa_score.cuh).
+float score_log2(float scale, float softcap) {
+  return (softcap > 0.0f ? softcap : scale) * 1.4426950408889634f;
+}
+
+template <Elt E, int kScore>
+fa_status launch_fwd_scored(int d, unsigned grid, cudaStream_t s, const CUtensorMap& mq,
+                            const CUtensorMap& mk, const CUtensorMap& mv, const fwd::Params& p) {
+  constexpr int T = fwd::kThreads;
+  if (d == 64)
+    return launch(fwd::fa_fwd_kernel<64, E, true, false, kScore>, grid, T,
+                  fwd::Cfg<64>::kSmemBytes, s, mq, mk, mv, p);
+  return launch(fwd::fa_fwd_kernel<128, E, true, false, kScore>, grid, T,
+                fwd::Cfg<128>::kSmemBytes, s, mq, mk, mv, p);
+}
+
+template <Elt E>
+fa_status forward_scored_impl(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                              int B, int H, int Hkv, int N, int d, float scale, int causal,
+                              int window_left, int window_right, float softcap,
+                              const float* slopes, const int32_t* documents, int n_docs,
+                              const int32_t* prefix, fa_stream_t stream) {
+  MaskSpec mask;
+  fwd::Params p;
+  fa_status st = check_shape(B, H, N, d, scale, causal);
+  if (st != FA_OK) return st;
+  if ((st = make_mask(N, causal, window_left, window_right, nullptr, &mask)) != FA_OK) return st;
+  if ((st = make_score(B, H, Hkv, scale, softcap, slopes, documents, n_docs, prefix, &p.score)) !=
+      FA_OK)
+    return st;
+  if (N == 0) return FA_OK;
+  if ((st = check_ptrs({Q, K, V, O, LSE})) != FA_OK) return st;
+  if ((st = prepare_device()) != FA_OK) return st;
+  const int BH = B * H;
+  CUtensorMap mq, mk, mv;
+  if (!make_map<E>(&mq, Q, BH, N, d, fwd::BM) || !make_map<E>(&mk, K, B * Hkv, N, d, fwd::BN) ||
+      !make_map<E>(&mv, V, B * Hkv, N, d, fwd::BN))
+    return FA_ERR_CUDA;
+  p.O = static_cast<uint16_t*>(O);
+  p.LSE = LSE;
+  p.N = N;
+  p.BH = BH;
+  const FwdSplit split = fwd_split(BH, N, d, mask.wl, mask.wr, false, device_sms(), false);
+  p.pairs_ph = split.pairs_ph;
+  p.singles_ph = split.singles_ph;
+  p.n_pair_items = BH * split.pairs_ph;
+  p.n_items = BH * (split.pairs_ph + split.singles_ph);
+  p.weight_major = split.weight_major;
+  p.scale_log2 = score_log2(scale, softcap);
+  p.wl = mask.wl;
+  p.wr = mask.wr;
+  p.blocks = nullptr;
+  p.n_kt = (N + fwd::BN - 1) / fwd::BN;
+  p.drop = DropoutParams{};
+  p.timeout_ns = watchdog_ns();
+  const unsigned grid = static_cast<unsigned>(p.n_items);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  constexpr int On = kScoreOn, Cap = kScoreCap, Bias = kScoreBias;
+  switch (score_bits(softcap, slopes)) {
+    case On: return launch_fwd_scored<E, On>(d, grid, s, mq, mk, mv, p);
+    case On | Cap: return launch_fwd_scored<E, On | Cap>(d, grid, s, mq, mk, mv, p);
+    case On | Bias: return launch_fwd_scored<E, On | Bias>(d, grid, s, mq, mk, mv, p);
+    default: return launch_fwd_scored<E, On | Cap | Bias>(d, grid, s, mq, mk, mv, p);
+  }
+}
+
+template <Elt E, int kScore>
+fa_status launch_bwd_scored(int d, unsigned grid, cudaStream_t s, const CUtensorMap& mq,
+                            const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                            const bwd::Params& p) {
+  constexpr int T = bwd::kThreads;
+  if (d == 64)
+    return launch(bwd::fa_bwd_kernel<64, E, true, false, kScore>, grid, T,
+                  bwd::Cfg<64>::kSmemBytes, s, mq, mk, mv, mdo, p);
+  return launch(bwd::fa_bwd_kernel<128, E, true, false, kScore>, grid, T,
+                bwd::Cfg<128>::kSmemBytes, s, mq, mk, mv, mdo, p);
+}
+
+template <Elt E>
+fa_status backward_scored_impl(const void* Q, const void* K, const void* V, const void* O,
+                               const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                               int B, int H, int Hkv, int N, int d, float scale, int causal,
+                               int window_left, int window_right, float softcap,
+                               const float* slopes, const int32_t* documents, int n_docs,
+                               const int32_t* prefix, void* workspace, size_t workspace_bytes,
+                               fa_stream_t stream) {
+  const void* ptrs[] = {Q, K, V, O, dO, LSE, dQ, dK, dV};
+  MaskSpec mask;
+  bwd::Params p;
+  BwdPlan pl;
+  fa_status st = check_shape(B, H, N, d, scale, causal);
+  if (st != FA_OK) return st;
+  if ((st = make_mask(N, causal, window_left, window_right, nullptr, &mask)) != FA_OK) return st;
+  if ((st = make_score(B, H, Hkv, scale, softcap, slopes, documents, n_docs, prefix, &p.score)) !=
+      FA_OK)
+    return st;
+  st = bwd_plan(ptrs, 9, B, H, N, d, scale, causal, workspace, workspace_bytes, &pl);
+  if (st != FA_OK || N == 0) return st;
+  st = preprocess_impl<E>(O, dO, LSE, B, H, N, d, scale, causal, workspace, workspace_bytes, stream);
+  if (st != FA_OK) return st;
+  CUtensorMap mq, mk, mv, mdo;
+  const int BHkv = B * Hkv;
+  if (!make_map<E>(&mq, Q, pl.BH, N, d, 64) || !make_map<E>(&mk, K, BHkv, N, d, bwd::BN) ||
+      !make_map<E>(&mv, V, BHkv, N, d, bwd::BN) || !make_map<E>(&mdo, dO, pl.BH, N, d, 64))
+    return FA_ERR_CUDA;
+  p.dK = static_cast<uint16_t*>(dK);
+  p.dV = static_cast<uint16_t*>(dV);
+  p.L2 = pl.L2;
+  p.Dv = pl.Dv;
+  p.dQacc = pl.dQacc;
+  p.N = N;
+  p.Npad = pl.Npad;
+  p.BH = BHkv;
+  p.scale = scale;
+  p.scale_log2 = score_log2(scale, softcap);
+  p.wl = mask.wl;
+  p.wr = mask.wr;
+  p.blocks = nullptr;
+  p.drop = DropoutParams{};
+  p.timeout_ns = watchdog_ns();
+  p.n_split = 0;
+  p.split_num = 8;
+  p.part = pl.part;
+  p.arrivals = pl.arrivals;
+  // the plain backward's rule for the order of the key tiles
+  const long long n_tiles = static_cast<long long>(BHkv) * (pl.Npad / bwd::BN);
+  p.rank_major = (mask.wr >= 0 || mask.wl >= 0) && n_tiles > device_sms() &&
+                         static_cast<double>(pl.BH) * N * d * 8.0 <= kBwdRankMajorBytes
+                     ? 1
+                     : 0;
+  const unsigned grid = static_cast<unsigned>(n_tiles);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  constexpr int On = kScoreOn, Cap = kScoreCap, Bias = kScoreBias;
+  switch (score_bits(softcap, slopes)) {
+    case On: st = launch_bwd_scored<E, On>(d, grid, s, mq, mk, mv, mdo, p); break;
+    case On | Cap: st = launch_bwd_scored<E, On | Cap>(d, grid, s, mq, mk, mv, mdo, p); break;
+    case On | Bias: st = launch_bwd_scored<E, On | Bias>(d, grid, s, mq, mk, mv, mdo, p); break;
+    default: st = launch_bwd_scored<E, On | Cap | Bias>(d, grid, s, mq, mk, mv, mdo, p);
+  }
+  if (st != FA_OK) return st;
+  return dq_convert_impl<E>(dQ, B, H, N, d, scale, workspace, workspace_bytes, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -919,6 +1120,25 @@ fa_status fa_launch_plan(int B, int H, int N, int d, int causal, int* fwd_persis
   if (fwd_persistent_out) *fwd_persistent_out = fp;
   if (bwd_persistent_out) *bwd_persistent_out = bp;
   if (bwd_split_out) *bwd_split_out = bs;
+  return FA_OK;
+}
+
+fa_status fa_score_span(const int32_t* documents, int n_docs, const int32_t* prefix, int N,
+                        int causal, int window_left, int window_right, int what, int index,
+                        int* lo, int* hi) {
+  if (N < 1 || N > (1 << 30) || index < 0 || index >= N || what < 0 || what > 3 ||
+      (causal != 0 && causal != 1) || lo == nullptr || hi == nullptr)
+    return FA_ERR_INVALID_ARG;
+  if (documents != nullptr && (n_docs < 1 || n_docs > (1 << 30))) return FA_ERR_INVALID_ARG;
+  MaskSpec m;
+  make_mask(N, causal, window_left, window_right, nullptr, &m);
+  if (documents == nullptr) n_docs = 1;
+  const Span s = what == 0   ? keys_of_query(documents, prefix, n_docs, N, m.wl, m.wr, index)
+                 : what == 1 ? queries_of_key(documents, prefix, n_docs, N, m.wl, m.wr, index)
+                 : what == 2 ? key_tiles_of_rows(documents, prefix, n_docs, N, m.wl, m.wr, index)
+                             : query_tiles_of_keys(documents, prefix, n_docs, N, m.wl, m.wr, index);
+  *lo = s.lo;
+  *hi = s.hi;
   return FA_OK;
 }
 
@@ -1134,6 +1354,52 @@ fa_status fa_backward_dropout_heads(const void* Q, const void* K, const void* V,
   if ((st = make_mask(N, causal, window_left, window_right, block_mask, &m)) != FA_OK) return st;
   return backward_impl<Elt::BF16>(Q, K, V, O, dO, LSE, dQ, dK, dV, B, H, N, d, scale, causal, m,
                                   dr, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_forward_scored(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                            int B, int H, int Hkv, int N, int d, float scale, int causal,
+                            int window_left, int window_right, float softcap,
+                            const float* slopes, const int32_t* documents, int n_docs,
+                            const int32_t* prefix, fa_stream_t stream) {
+  return forward_scored_impl<Elt::BF16>(Q, K, V, O, LSE, B, H, Hkv, N, d, scale, causal, window_left,
+                                       window_right, softcap, slopes, documents, n_docs, prefix,
+                                       stream);
+}
+
+fa_status fa_backward_scored(const void* Q, const void* K, const void* V, const void* O,
+                             const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                             int B, int H, int Hkv, int N, int d, float scale, int causal,
+                             int window_left, int window_right, float softcap,
+                             const float* slopes, const int32_t* documents, int n_docs,
+                             const int32_t* prefix, void* workspace, size_t workspace_bytes,
+                             fa_stream_t stream) {
+  return backward_scored_impl<Elt::BF16>(Q, K, V, O, dO, LSE, dQ, dK, dV, B, H, Hkv, N, d, scale,
+                                        causal, window_left, window_right, softcap, slopes,
+                                        documents, n_docs, prefix, workspace, workspace_bytes,
+                                        stream);
+}
+
+fa_status fa_forward_scored_f16(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                            int B, int H, int Hkv, int N, int d, float scale, int causal,
+                            int window_left, int window_right, float softcap,
+                            const float* slopes, const int32_t* documents, int n_docs,
+                            const int32_t* prefix, fa_stream_t stream) {
+  return forward_scored_impl<Elt::F16>(Q, K, V, O, LSE, B, H, Hkv, N, d, scale, causal, window_left,
+                                       window_right, softcap, slopes, documents, n_docs, prefix,
+                                       stream);
+}
+
+fa_status fa_backward_scored_f16(const void* Q, const void* K, const void* V, const void* O,
+                             const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                             int B, int H, int Hkv, int N, int d, float scale, int causal,
+                             int window_left, int window_right, float softcap,
+                             const float* slopes, const int32_t* documents, int n_docs,
+                             const int32_t* prefix, void* workspace, size_t workspace_bytes,
+                             fa_stream_t stream) {
+  return backward_scored_impl<Elt::F16>(Q, K, V, O, dO, LSE, dQ, dK, dV, B, H, Hkv, N, d, scale,
+                                        causal, window_left, window_right, softcap, slopes,
+                                        documents, n_docs, prefix, workspace, workspace_bytes,
+                                        stream);
 }
 
 fa_status fa_forward_f32(const float* Q, const float* K, const float* V, float* O, float* LSE,

@@ -1,0 +1,205 @@
+// fa_score.cuh -- shaped scores: what the forward, the backward and the attention over a
+// 4-bit cache share. A score is
+//   t = cap * tanh(scale * q.k / cap) - slope_h * |i - j|   (either term may be off),
+// and query i sees key j iff both lie in one document, i - wl <= j (wl >= 0), and
+// j <= i + wr (wr >= 0; causal is wr = 0) or j lies in the document's prefix.
+//
+// Documents are runs of a row given by their offsets, so the keys that a query sees, and
+// the queries that see a key, are intervals, and both ends of the interval grow with the
+// row index. The kernels use that twice: the tiles that a block of rows walks are those
+// from its first row's lower end to its last row's upper end, and a tile needs no element
+// test where it lies between the last row's lower end and the first row's upper end.
+#pragma once
+
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+// Bits of the kernels' kScore parameter (0: plain scores, nothing of this file is used).
+constexpr int kScoreOn = 1;    // documents, prefix, shared K/V heads
+constexpr int kScoreCap = 2;   // tanh cap
+constexpr int kScoreBias = 4;  // distance bias
+
+struct ScoreParams {
+  const float* slopes;  // [H], or null
+  const int* docs;      // [B, n_docs + 1] offsets, or null: one document [0, N)
+  const int* prefix;    // [B, n_docs] prefix lengths, or null
+  int n_docs;           // >= 1
+  int H;                // query heads per batch entry
+  int group;            // query heads that share a K/V head
+  // tanh(x) = s * q(s^2) with x = s * scale / cap: q's coefficients with the powers of
+  // scale / cap folded in, and the bound on s^2 up to which it holds (see make_score)
+  float q[5];
+  float lim2;
+  float cap_in2;      // 2 * log2(e) * scale / cap, for the form on the exponential
+  float slope_mul;    // a slope times this is in units of the scores before c (below)
+};
+
+// tanh(x) / x as a polynomial in x^2 on |x| <= 0.7: least squares at Chebyshev nodes with
+// Lawson reweighting toward the minimax fit; largest relative error 3.1e-7.
+constexpr float kTanhLimit = 0.7f;
+constexpr double kTanhQ[5] = {0.9999996973, -0.3333021293, 0.1328111269, -0.05083623683,
+                              0.01377370979};
+
+struct Span {
+  int lo, hi;
+};
+
+// The document of token i: the last m with offsets[m] <= i (so empty documents are passed
+// over), or -1 in front of the first. n_docs: behind the last. Ends for any contents.
+__host__ __device__ __forceinline__ int doc_of(const int* offsets, int n_docs, int i) {
+  int a = -1, b = n_docs + 1;  // offsets[a] <= i < offsets[b], with -inf and +inf at the ends
+  while (b - a > 1) {
+    const int m = (a + b) >> 1;
+    if (offsets[m] <= i) a = m; else b = m;
+  }
+  return a;
+}
+
+// Token i's document [s, e) within [0, N) and the end of its prefix; an empty document
+// for padding. docs and prefix are the batch entry's own rows.
+__host__ __device__ __forceinline__ void doc_span(const int* docs, const int* prefix, int n_docs,
+                                                  int N, int i, int& s, int& e, int& ahead) {
+  int m = 0;
+  s = 0;
+  e = N;
+  if (docs != nullptr) {
+    m = doc_of(docs, n_docs, i);
+    if (m < 0 || m >= n_docs) {
+      s = e = ahead = 0;
+      return;
+    }
+    s = docs[m] < 0 ? 0 : docs[m];
+    e = docs[m + 1] > N ? N : docs[m + 1];
+    if (e < s) e = s;
+  }
+  int p = prefix != nullptr ? prefix[m] : 0;
+  p = p < 0 ? 0 : (p > e - s ? e - s : p);
+  ahead = s + p;
+}
+
+// Keys [lo, hi) that query i sees; empty for i >= N and for padding.
+__host__ __device__ __forceinline__ Span keys_of_query(const int* docs, const int* prefix,
+                                                       int n_docs, int N, int wl, int wr, int i) {
+  if (i < 0 || i >= N) return Span{0, 0};
+  int s, e, ahead;
+  doc_span(docs, prefix, n_docs, N, i, s, e, ahead);
+  Span k{s, e};
+  if (wl >= 0 && i - wl > k.lo) k.lo = i - wl;
+  if (wr >= 0) {
+    const int r = i + wr + 1 > ahead ? i + wr + 1 : ahead;
+    if (r < k.hi) k.hi = r;
+  }
+  if (k.hi < k.lo) k.hi = k.lo;
+  return k;
+}
+
+// Queries [lo, hi) that see key j; empty for j >= N and for padding.
+__host__ __device__ __forceinline__ Span queries_of_key(const int* docs, const int* prefix,
+                                                        int n_docs, int N, int wl, int wr, int j) {
+  if (j < 0 || j >= N) return Span{0, 0};
+  int s, e, ahead;
+  doc_span(docs, prefix, n_docs, N, j, s, e, ahead);
+  Span q{s, e};
+  if (wr >= 0 && j >= ahead && j - wr > q.lo) q.lo = j - wr;
+  if (wl >= 0 && j + wl + 1 < q.hi) q.hi = j + wl + 1;
+  if (q.hi < q.lo) q.hi = q.lo;
+  return q;
+}
+
+// The first and last tokens of rows [r0, r1] that lie in a document (first > last if none).
+__host__ __device__ __forceinline__ void real_rows(const int* docs, int n_docs, int N, int r0,
+                                                   int r1, int& first, int& last) {
+  first = r0;
+  last = r1 < N - 1 ? r1 : N - 1;
+  if (docs != nullptr) {
+    if (docs[0] > first) first = docs[0];
+    if (docs[n_docs] - 1 < last) last = docs[n_docs] - 1;
+  }
+}
+
+// 128-wide tiles [lo, hi) that hold every key some query of rows [r0, r0 + 127] sees.
+__host__ __device__ __forceinline__ Span key_tiles_of_rows(const int* docs, const int* prefix,
+                                                           int n_docs, int N, int wl, int wr,
+                                                           int r0) {
+  int first, last;
+  real_rows(docs, n_docs, N, r0, r0 + 127, first, last);
+  if (first > last) return Span{0, 0};
+  const Span a = keys_of_query(docs, prefix, n_docs, N, wl, wr, first);
+  const Span b = keys_of_query(docs, prefix, n_docs, N, wl, wr, last);
+  if (b.hi <= a.lo) return Span{0, 0};
+  return Span{a.lo / 128, (b.hi + 127) / 128};
+}
+
+// 128-wide tiles [lo, hi) that hold every query that sees some key of rows [r0, r0 + 127].
+__host__ __device__ __forceinline__ Span query_tiles_of_keys(const int* docs, const int* prefix,
+                                                             int n_docs, int N, int wl, int wr,
+                                                             int r0) {
+  int first, last;
+  real_rows(docs, n_docs, N, r0, r0 + 127, first, last);
+  if (first > last) return Span{0, 0};
+  const Span a = queries_of_key(docs, prefix, n_docs, N, wl, wr, first);
+  const Span b = queries_of_key(docs, prefix, n_docs, N, wl, wr, last);
+  if (b.hi <= a.lo) return Span{0, 0};
+  return Span{a.lo / 128, (b.hi + 127) / 128};
+}
+
+// tanh of a pair of scores on the FMA pipe, for s^2 <= lim2 (given as S = s * s).
+__device__ __forceinline__ float2 tanh_poly2(float2 s, float2 S, const ScoreParams& p) {
+  float2 r = ffma2(S, make_float2(p.q[4], p.q[4]), make_float2(p.q[3], p.q[3]));
+  r = ffma2(r, S, make_float2(p.q[2], p.q[2]));
+  r = ffma2(r, S, make_float2(p.q[1], p.q[1]));
+  r = ffma2(r, S, make_float2(p.q[0], p.q[0]));
+  return fmul2(s, r);
+}
+
+// tanh of one score of any size: 1 - 2 / (1 + e^2x), by the exponential and the reciprocal
+// of the MUFU unit. Absolute error about 2e-7, which the cap multiplies: fit for |x| of the
+// order of one and more, where the polynomial does not reach.
+__device__ __forceinline__ float tanh_exp(float s, float cap_in2) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(s * cap_in2)));
+  return fmaf(-2.0f, r, 1.0f);
+}
+
+// tanh in place of n scores held by this thread (n even). Which form is a warp's choice
+// (the branch would diverge otherwise): the polynomial where every score of the warp's
+// piece lies within its reach. Capped models keep most scores well inside the cap.
+template <int n>
+__device__ __forceinline__ void tanh_scores(uint32_t (&s)[n], const ScoreParams& p) {
+  float2 S[n / 2];
+  float top = 0.0f;
+#pragma unroll
+  for (int k = 0; k < n / 2; ++k) {
+    const float2 x = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+    S[k] = fmul2(x, x);
+    top = fmax3(top, S[k].x, S[k].y);
+  }
+  if (__any_sync(0xffffffffu, !(top <= p.lim2))) {
+#pragma unroll
+    for (int k = 0; k < n; ++k)
+      s[k] = __float_as_uint(tanh_exp(__uint_as_float(s[k]), p.cap_in2));
+  } else {
+#pragma unroll
+    for (int k = 0; k < n / 2; ++k) {
+      const float2 r = tanh_poly2(
+          make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), S[k], p);
+      s[2 * k] = __float_as_uint(r.x);
+      s[2 * k + 1] = __float_as_uint(r.y);
+    }
+  }
+}
+
+// Subtracts the distance bias in place from n scores of consecutive columns: score k gets
+// slope_neg * |d0 + k| added, d0 the (whole) distance of column 0 from this thread's row.
+// Distances below 2^24 are exact in 32 bits.
+template <int n>
+__device__ __forceinline__ void bias_scores(uint32_t (&s)[n], int d0, float slope_neg) {
+  const float f0 = static_cast<float>(d0);
+#pragma unroll
+  for (int k = 0; k < n; ++k)
+    s[k] = __float_as_uint(
+        fmaf(slope_neg, fabsf(f0 + static_cast<float>(k)), __uint_as_float(s[k])));
+}
+
+}  // namespace fa

@@ -1,0 +1,245 @@
+"""Attention with shaped scores on the GPU against its 64-bit definition, within the bounds
+that follow from its roundings (score_reference.gradients). Outputs are filled with NaN
+before each call, the workspace with 0xFF."""
+import math
+
+import pytest
+import torch
+
+import score_reference as ref
+from io_aware_attention_flashattention_b200 import api
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+def make(B, H, Hkv, N, d, dtype, seed, gain=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda h, a=1.0: (torch.randn(B, h, N, d, generator=g, device="cuda") * a).to(dtype)  # noqa: E731
+    return n(H, gain), n(Hkv), n(Hkv), n(H)
+
+
+def options(case, B, H, N):
+    kw = {}
+    if case.get("slopes"):
+        kw["slopes"] = torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)], device="cuda")
+    if "documents" in case:
+        kw["documents"] = torch.tensor(case["documents"], dtype=torch.int32, device="cuda")
+    if "prefix" in case:
+        kw["prefix"] = torch.tensor(case["prefix"], dtype=torch.int32, device="cuda")
+    if "softcap" in case:
+        kw["softcap"] = case["softcap"]
+    return kw
+
+
+def run(q, k, v, do, scale, causal, window, kw):
+    suffix = "_f16" if q.dtype == HF else ""
+    nan = lambda t: torch.full_like(t, float("nan"))  # noqa: E731
+    o, lse = nan(q), torch.full(q.shape[:3], float("nan"), device="cuda")
+    getattr(api, "fa_forward_scored" + suffix)(q, k, v, o, lse, scale, causal, window, **kw)
+    dq, dk, dv = nan(q), nan(k), nan(v)
+    ws = api.workspace_for(q).fill_(0xFF)
+    getattr(api, "fa_backward_scored" + suffix)(q, k, v, o, do, lse, dq, dk, dv, scale, causal, ws, window, **kw)
+    torch.cuda.synchronize()
+    assert api.fa_get_status() == 0
+    return o, lse, dq, dk, dv
+
+
+def check(got, q, k, v, do, mask, scale, softcap, slopes):
+    values, bounds = ref.gradients(q, k, v, do, mask.cuda(), scale, softcap, slopes)
+    for name, g, w, b in zip(("O", "LSE", "dQ", "dK", "dV"), got, values, bounds):
+        g = g.double()
+        empty = ~torch.isfinite(w) if name == "LSE" else None
+        if empty is not None:
+            assert torch.equal(g == -math.inf, empty), "rows that see nothing"
+            g, w, b = g[~empty], w[~empty], b[~empty]
+        if name == "O":  # rows that see nothing are 0, exactly
+            none = ~mask.any(-1)[:, None].expand(w.shape[:3]).cuda()
+            assert (g[none] == 0).all()
+            w = torch.where(none[..., None], torch.zeros_like(w), w)
+            b = torch.where(none[..., None], torch.zeros_like(b), b)
+        assert torch.isfinite(g).all(), name
+        over = (g - w).abs() - b
+        assert g.numel() == 0 or over.max() <= 0, f"{name}: {float(over.max()):.3g} over its bound, error " \
+            f"{float((g - w).abs().max()):.3g}"
+        if name in ("dQ", "dK", "dV"):
+            dead = (mask.any(-1) if name == "dQ" else mask.any(1))[:, None].expand(g.shape[:3]).cuda()
+            assert (g[~dead] == 0).all(), f"{name} of what sees nothing"
+
+
+CASES = [
+    # B, H, Hkv, N, d, type, causal, window, the rest
+    (1, 1, 1, 1, 64, BF, True, (-1, -1), dict(softcap=50.0)),
+    (2, 2, 1, 2, 128, HF, False, (-1, -1), dict(softcap=5.0, slopes=True)),
+    (1, 2, 2, 77, 128, BF, True, (-1, -1), dict(softcap=50.0)),
+    (1, 4, 2, 129, 64, BF, True, (-1, -1), dict(slopes=True)),
+    (2, 4, 1, 200, 128, HF, False, (-1, -1), dict(slopes=True)),
+    (1, 3, 3, 384, 128, BF, False, (-1, -1), dict(softcap=20.0)),
+    (1, 6, 2, 500, 64, HF, True, (40, -1), dict(softcap=30.0, slopes=True)),
+    (1, 2, 1, 700, 128, BF, False, (130, 70), dict(softcap=30.0, slopes=True)),
+    (1, 4, 4, 300, 64, BF, True, (-1, -1), {}),
+    (2, 8, 2, 300, 128, BF, True, (-1, -1), {}),
+    (2, 2, 1, 300, 128, BF, True, (-1, -1), dict(documents=[[0, 1, 1, 130, 299], [3, 60, 200, 256, 257]])),
+    (2, 4, 2, 513, 64, HF, False, (-1, -1), dict(documents=[[0, 513], [500, 500]], slopes=True)),
+    (2, 2, 2, 400, 64, BF, True, (-1, -1), dict(prefix=[200, 0])),
+    (1, 2, 2, 640, 128, BF, True, (100, -1), dict(documents=[[0, 128, 256, 640]], prefix=[[128, 5, 300]])),
+    (2, 4, 1, 450, 128, HF, True, (-1, -1), dict(documents=[[0, 7, 300, 400], [0, 0, 0, 450]],
+                                                 prefix=[[7, 150, 0], [0, 0, 129]], softcap=15.0, slopes=True)),
+    (1, 2, 1, 1000, 64, BF, False, (-1, 64), dict(documents=[[128, 384, 896]], prefix=[[256, 256]])),
+    (3, 2, 2, 260, 64, BF, True, (-1, -1), dict(documents=[[0, 0], [260, 260], [0, 260]])),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x) for x in c[:6]))
+def test_forward_and_backward(case):
+    B, H, Hkv, N, d, dtype, causal, window, rest = case
+    q, k, v, do = make(B, H, Hkv, N, d, dtype, seed=N)
+    scale = 1.0 / math.sqrt(d)
+    kw = options(rest, B, H, N)
+    got = run(q, k, v, do, scale, causal, window, kw)
+    mask = ref.visible(B, N, causal, window, rest.get("documents"),
+                       torch.tensor(rest["prefix"]) if "prefix" in rest else None)
+    check(got, q, k, v, do, mask, scale, rest.get("softcap"), kw.get("slopes"))
+
+
+@pytest.mark.parametrize("cap,gain", [(0.01, 1.0), (1.0, 4.0), (5.0, 30.0), (50.0, 60.0), (1e4, 1.0), (1e6, 8.0)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_caps_far_from_the_scores_size(cap, gain, dtype):
+    """Scores well inside, around and far beyond the cap: both forms of tanh, and their seam."""
+    q, k, v, do = make(1, 2, 1, 190, 64, dtype, seed=int(cap) + 1, gain=gain)
+    got = run(q, k, v, do, 0.125, True, None, dict(softcap=cap))
+    check(got, q, k, v, do, ref.visible(1, 190, True), 0.125, cap, None)
+
+
+def test_infinite_scores_meet_the_cap():
+    """A score beyond 32 bits' range is capped like any large one."""
+    q, k, v, do = make(1, 1, 1, 64, 64, BF, seed=3)
+    q[0, 0, 5], k[0, 0, 3] = 0.0, 0.0
+    q[0, 0, 5, 0], k[0, 0, 3, 0] = 3e38, 3e38
+    o, lse, *_ = run(q, k, v, do, 0.125, True, None, dict(softcap=10.0))
+    assert torch.isfinite(o[0, 0, :3]).all() and torch.isfinite(lse).all()
+    w = torch.tanh((q[0, 0, 5].double() @ k[0, 0, :6].double().T) * 0.125 / 10.0) * 10.0
+    assert abs(float(lse[0, 0, 5]) - float(torch.logsumexp(w, 0))) < 1e-4
+
+
+def test_documents_match_separate_calls_bit_for_bit_in_the_forward():
+    """A packed row equals its documents run one by one, where they start on a tile."""
+    q, k, v, do = make(1, 4, 2, 640, 128, BF, seed=8)
+    docs = [0, 128, 512, 640]
+    o, lse = api.forward(q, k, v, causal=True, documents=torch.tensor([docs], dtype=torch.int32, device="cuda"))
+    for s, e in zip(docs, docs[1:]):
+        part = [x[:, :, s:e].contiguous() for x in (q, k, v)]
+        a, b = api.forward(*part, causal=True)
+        assert torch.equal(o[:, :, s:e], a) and torch.equal(lse[:, :, s:e], b)
+
+
+def test_off_terms_give_the_plain_calls_results():
+    """No cap, one document, no prefix: bit for bit the plain forward, and dK, dV as well."""
+    q, k, v, do = make(2, 3, 3, 300, 64, HF, seed=9)
+    one = torch.tensor([[0, 300]] * 2, dtype=torch.int32, device="cuda")
+    o, lse = api.forward(q, k, v, causal=True, documents=one)
+    a, b = api.forward(q, k, v, causal=True)
+    assert torch.equal(o, a) and torch.equal(lse, b)
+    got = api.backward(q, k, v, o, lse, do, causal=True, documents=one)
+    want = api.backward(q, k, v, o, lse, do, causal=True)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+def test_autograd_shared_heads_and_strides():
+    """attention() through autograd, from tensors laid out as projections leave them."""
+    B, H, Hkv, N, d = 2, 4, 2, 150, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = [torch.randn(B, N, h, d, generator=g, device="cuda").to(BF).requires_grad_() for h in (H, Hkv, Hkv)]
+    q, k, v = (t.transpose(1, 2) for t in x)
+    docs = torch.tensor([[0, 20, 150], [0, 90, 140]], dtype=torch.int32, device="cuda")
+    slopes = torch.tensor([0.5, 0.25, 0.125, 0.0625], device="cuda")
+    kw = dict(softcap=12.0, slopes=slopes, documents=docs, prefix=torch.tensor([[5, 0], [0, 7]], dtype=torch.int32,
+                                                                               device="cuda"))
+    o = api.attention(q, k, v, causal=True, **kw)
+    do = torch.randn(o.shape, generator=g, device="cuda").to(BF)
+    grads = torch.autograd.grad(o, x, do)
+    mask = ref.visible(B, N, True, documents=docs.tolist(), prefix=kw["prefix"].cpu())
+    values, bounds = ref.gradients(q.detach(), k.detach(), v.detach(), do, mask.cuda(), 1 / math.sqrt(d), 12.0, slopes)
+    for got, want, b in zip(grads, values[2:], bounds[2:]):
+        assert ((got.transpose(1, 2).double() - want).abs() <= b).all()
+
+
+def test_captured_training_step_replays_and_other_stream():
+    """A captured forward and backward, replayed on new inputs and beside an eager call on
+    another stream, gives what the calls give one by one."""
+    B, H, Hkv, N, d = 1, 4, 2, 333, 64
+    sets = [make(B, H, Hkv, N, d, BF, seed=s) for s in (1, 2, 3)]
+    docs = torch.tensor([[0, 100, 320]], dtype=torch.int32, device="cuda")
+    kw = dict(causal=True, softcap=20.0, documents=docs)
+
+    def step(q, k, v, do):
+        o, lse = api.forward(q, k, v, **kw)
+        return (o, lse) + api.backward(q, k, v, o, lse, do, **kw)
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    held = [t.clone() for t in sets[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*held)
+    side = torch.cuda.Stream()
+    for s, w in zip(sets, want):
+        for a, b in zip(held, s):
+            a.copy_(b)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            other = step(*sets[0])
+        torch.cuda.synchronize()
+        for n, (a, b) in enumerate(zip(out, w)):
+            if n == 2:  # dQ: fp32 atomic adds in some order
+                assert ((a.float() - b.float()).abs() <= 2.0 ** -6 * b.float().abs() + 1e-5).all()
+            else:
+                assert torch.equal(a, b)
+        assert torch.equal(other[3], want[0][3])
+    assert api.fa_get_status() == 0
+
+
+def test_long_row_against_sampled_rows():
+    """16384 tokens, one head of each kind: sampled rows of O, dQ against 64 bits."""
+    N, d = 16384, 128
+    q, k, v, do = make(1, 2, 1, N, d, BF, seed=11, gain=4.0)
+    o, lse = api.forward(q, k, v, causal=True, softcap=50.0)
+    dq, dk, dv = api.backward(q, k, v, o, lse, do, causal=True, softcap=50.0)
+    u = 2.0 ** -8
+    for i in (0, 1, 127, 128, 5000, N - 1):
+        x = torch.tanh((k[0, 0, :i + 1].double() @ q[0, 1, i].double()) / math.sqrt(d) / 50.0)
+        t = 50.0 * x
+        p = torch.softmax(t, 0)
+        val = p @ v[0, 0, :i + 1].double()
+        size = p @ v[0, 0, :i + 1].double().abs()
+        b_o = 3.2 * u * size + u * val.abs()
+        assert ((o[0, 1, i].double() - val).abs() <= b_o).all()
+        g = do[0, 1, i].double()
+        ds = p * (v[0, 0, :i + 1].double() @ g - g @ val) * (1 - x * x) / math.sqrt(d)
+        want = ds @ k[0, 0, :i + 1].double()
+        b = (p * float(g.abs() @ b_o) / math.sqrt(d) + 2.2 * u * ds.abs()) @ k[0, 0, :i + 1].double().abs()
+        assert ((dq[0, 1, i].double() - want).abs() <= 1.05 * b + u * want.abs()).all()
+
+
+def test_offsets_beyond_32_bits():
+    """Query heads whose rows lie past element 2^31 (520 heads of 32768 x 128)."""
+    H, N, d = 520, 32768, 128
+    q = torch.zeros(1, H, N, d, dtype=BF, device="cuda")
+    q[0, -1] = torch.randn(N, d, device="cuda").to(BF)
+    k = torch.randn(1, 1, N, d, device="cuda").to(BF)
+    v = torch.randn(1, 1, N, d, device="cuda").to(BF)
+    o, lse = api.forward(q, k, v, causal=True, window=(255, -1), softcap=50.0)
+    torch.cuda.synchronize()
+    assert api.fa_get_status() == 0
+    for i in (0, 300, N - 1):
+        lo = max(0, i - 255)
+        t = 50.0 * torch.tanh((k[0, 0, lo:i + 1].double() @ q[0, -1, i].double()) / math.sqrt(d) / 50.0)
+        p = torch.softmax(t, 0)
+        val = p @ v[0, 0, lo:i + 1].double()
+        b = 2.0 ** -8 * (3.2 * (p @ v[0, 0, lo:i + 1].double().abs()) + val.abs())
+        assert ((o[0, -1, i].double() - val).abs() <= b).all()
+        assert abs(float(lse[0, -1, i]) - float(torch.logsumexp(t, 0))) < 1e-3
+    del q, o
+    torch.cuda.empty_cache()
