@@ -69,7 +69,8 @@ typedef enum {
   FA_ERR_INVALID_ARG = 1, /* null/misaligned pointer, bad shape, bad scale */
   FA_ERR_UNSUPPORTED = 2, /* valid arguments outside what this library implements */
   FA_ERR_CUDA = 3,        /* a CUDA call or launch failed (no device, bad context) */
-  FA_ERR_TIMEOUT = 4      /* a kernel's bounded wait ran out (see fa_get_status) */
+  FA_ERR_TIMEOUT = 4,     /* a kernel's bounded wait ran out (see fa_get_status) */
+  FA_ERR_BAD_PAGE = 5     /* a cache call met a position without a page (see fa_get_status) */
 } fa_status;
 
 /*
@@ -328,6 +329,86 @@ fa_status fa_score_span(const int32_t* documents, int n_docs, const int32_t* pre
                         int* lo, int* hi);
 
 /*
+ * A key/value cache held in 4 bits (bf16 model tensors; f16 with the suffix _f16).
+ *
+ * A row, one token's K or V of one head (d values, d in {64, 128}), is held as codes of 4
+ * bits and a pair (scale, zero) in the model's 16-bit type:
+ *   zero = min x, scale = max x / 15 - min x / 15 rounded to the type,
+ *   code = round((x - zero) / scale) to nearest even, within 0..15 (0 where scale is 0),
+ *   value = scale * code + zero.
+ *   codes:  DEVICE bytes [n_pages, 2, Hkv, page, d / 2] (index 0 of the second axis K, 1 V);
+ *           channel 2c is the low half of byte c, channel 2c + 1 the high half.
+ *   params: DEVICE [n_pages, 2, Hkv, page, 2] of the model's type, (scale, zero).
+ *   page:   tokens per page, one of 16, 32, 64, 128, 256; max_pages * page < 2^31.
+ *   page_table: DEVICE int32 [B, max_pages]; token t of sequence b lies in slot t % page of
+ *           page page_table[b][t / page]. Entries that no token needs may hold anything.
+ * Base addresses of codes and params are 16-byte aligned. Sequences may share pages that
+ * they only read. A token whose position lies outside the table, or whose entry lies outside
+ * [0, n_pages), is passed over (not written, read as zeros, not attended) and noted in the
+ * status word: fa_get_status() then returns FA_ERR_BAD_PAGE.
+ *
+ * fa_cache4_append: K, V [B, Hkv, n, d] into the cache: token t < counts[b] of sequence b
+ *   goes to position positions[b] + t. counts (DEVICE int32 [B]) may be NULL: n each; larger
+ *   counts count as n. Nothing else of the cache changes. Rows must be finite: a row with
+ *   a NaN reads back as NaN, one with an infinity has undefined values.
+ * fa_cache4_read: the same rows back, into K, V [B, Hkv, n, d]; rows t >= counts[b] are 0.
+ */
+fa_status fa_cache4_append(const void* K, const void* V, void* codes, void* params,
+                          const int32_t* page_table, const int32_t* positions,
+                          const int32_t* counts, int B, int Hkv, int n, int d, int page,
+                          int64_t n_pages, int max_pages, fa_stream_t stream);
+fa_status fa_cache4_read(void* K, void* V, const void* codes, const void* params,
+                        const int32_t* page_table, const int32_t* positions,
+                        const int32_t* counts, int B, int Hkv, int n, int d, int page,
+                        int64_t n_pages, int max_pages, fa_stream_t stream);
+fa_status fa_cache4_append_f16(const void* K, const void* V, void* codes, void* params,
+                          const int32_t* page_table, const int32_t* positions,
+                          const int32_t* counts, int B, int Hkv, int n, int d, int page,
+                          int64_t n_pages, int max_pages, fa_stream_t stream);
+fa_status fa_cache4_read_f16(void* K, void* V, const void* codes, const void* params,
+                        const int32_t* page_table, const int32_t* positions,
+                        const int32_t* counts, int B, int Hkv, int n, int d, int page,
+                        int64_t n_pages, int max_pages, fa_stream_t stream);
+
+/*
+ * Attention of the last Nq tokens of each sequence over a 4-bit cache (which holds those
+ * tokens too): O and LSE as for fa_forward_scored of query n at position
+ * lengths[b] - Nq + n over the keys at positions up to its own, with Q, O [B, H, Nq, d] and
+ * LSE fp32 [B, H, Nq]; query head h reads K/V head h / (H / Hkv).
+ *   lengths: DEVICE int32 [B]; at most max_pages * page (more is cut there, and noted as
+ *     FA_ERR_BAD_PAGE). A query whose position is negative sees nothing: O = 0, LSE = -inf.
+ *   max_len: a bound on the lengths, known on the host; it only sizes the launch, and the
+ *     result does not depend on it beyond rounding.
+ *   window_left: keys before position - window_left are not seen; negative: no window.
+ *   softcap, slopes: as for fa_forward_scored.
+ *   workspace: fa_cache4_workspace_size(B, H, Hkv, Nq, d, min(max_len, max_pages * page),
+ *     window_left) bytes, 16-byte aligned; may be NULL where that is 0. Its contents do not
+ *     matter and are undefined on return; calls that may overlap need one each.
+ * The result is the same from run to run. Nq = 0 is a no-op.
+ */
+fa_status fa_cache4_attend(const void* Q, void* O, float* LSE, const void* codes,
+                          const void* params, const int32_t* page_table, const int32_t* lengths,
+                          int B, int H, int Hkv, int Nq, int d, int page, int64_t n_pages,
+                          int max_pages, int max_len, float scale, int window_left,
+                          float softcap, const float* slopes, void* workspace,
+                          size_t workspace_bytes, fa_stream_t stream);
+fa_status fa_cache4_attend_f16(const void* Q, void* O, float* LSE, const void* codes,
+                          const void* params, const int32_t* page_table, const int32_t* lengths,
+                          int B, int H, int Hkv, int Nq, int d, int page, int64_t n_pages,
+                          int max_pages, int max_len, float scale, int window_left,
+                          float softcap, const float* slopes, void* workspace,
+                          size_t workspace_bytes, fa_stream_t stream);
+size_t fa_cache4_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int window_left);
+
+/*
+ * Row index (of d / 2 bytes of codes and of one pair of params) of token `token` of a
+ * sequence with the HOST page table row given, or -1 for a token without a page or bad
+ * arguments. Host only.
+ */
+int64_t fa_cache4_row(const int32_t* page_table_row, int max_pages, int64_t n_pages, int Hkv,
+                      int page, int which, int head, int64_t token);
+
+/*
  * The drop probability the dropout calls apply for `p_drop`: floor(256 p_drop) / 256
  * (for example 0.1 gives 25/256 = 0.09765625). Returns -1 for a p_drop those calls
  * refuse (outside [0, 1), NaN, or in (0, 1/256)). Host only; no CUDA call.
@@ -366,6 +447,8 @@ fa_status fa_backward_f32(const float* Q, const float* K, const float* V, const 
 /*
  * Synchronises `stream`, reads and clears the device status word of the current
  * GPU. Returns FA_ERR_TIMEOUT if a kernel since the last call gave up on a wait,
+ * FA_ERR_BAD_PAGE if a cache call met a token whose page table entry lies outside the
+ * cache (or whose position lies outside the table),
  * FA_ERR_CUDA if the synchronisation itself failed, else FA_OK.
  */
 fa_status fa_get_status(fa_stream_t stream);

@@ -12,16 +12,19 @@ from .build import LIB
 _lock = threading.Lock()
 _handle = None
 
-FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
+FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_BAD_PAGE = range(6)
 
 # name -> (restype, argtypes), exactly the declarations of include/fa.h
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-_u32, _u64 = ctypes.c_uint32, ctypes.c_uint64
+_u32, _u64, _i64 = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int64
 # B, H, Hkv, N, d, scale, causal, window_left, window_right, softcap, slopes, documents, n_docs,
 # prefix
 _SCORE = [_i, _i, _i, _i, _i, _f, _i, _i, _i, _f, _vp, _vp, _i, _vp]
 _SCORED_FWD = (_i, [_vp] * 5 + _SCORE + [_vp])
 _SCORED_BWD = (_i, [_vp] * 9 + _SCORE + [_vp, _sz, _vp])
+# ..., B, Hkv, n, d, page, n_pages, max_pages, stream
+_CACHE4_ROWS = (_i, [_vp] * 7 + [_i] * 5 + [_i64, _i, _vp])
+_CACHE4_ATTEND = (_i, [_vp] * 7 + [_i] * 6 + [_i64, _i, _i, _f, _i, _f, _vp, _vp, _sz, _vp])
 SIGNATURES = {
     "fa_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_backward_workspace_size": (_sz, [_i, _i, _i, _i]),
@@ -59,6 +62,14 @@ SIGNATURES = {
     "fa_backward_scored": _SCORED_BWD,
     "fa_forward_scored_f16": _SCORED_FWD,
     "fa_backward_scored_f16": _SCORED_BWD,
+    "fa_cache4_append": _CACHE4_ROWS,
+    "fa_cache4_read": _CACHE4_ROWS,
+    "fa_cache4_attend": _CACHE4_ATTEND,
+    "fa_cache4_append_f16": _CACHE4_ROWS,
+    "fa_cache4_read_f16": _CACHE4_ROWS,
+    "fa_cache4_attend_f16": _CACHE4_ATTEND,
+    "fa_cache4_workspace_size": (_sz, [_i] * 7),
+    "fa_cache4_row": (_i64, [_vp, _i, _i64, _i, _i, _i, _i, _i64]),
     "fa_score_span": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp]),
     "fa_get_status": (_i, [_vp]),
     "fa_watchdog_selftest": (_i, [_i, _vp]),

@@ -29,9 +29,11 @@ __all__ = [
     "fa_backward_noalloc", "fa_forward_f16", "fa_backward_f16", "fa_forward_masked",
     "fa_backward_masked", "fa_forward_dropout", "fa_backward_dropout", "fa_forward_f32",
     "fa_backward_f32", "fa_forward_scored", "fa_backward_scored", "fa_forward_scored_f16",
-    "fa_backward_scored_f16", "fa_get_status", "fa_watchdog_selftest", "fa_version", "fa_dropout_rate",
+    "fa_backward_scored_f16", "fa_cache4_append", "fa_cache4_read", "fa_cache4_attend",
+    "fa_cache4_append_f16", "fa_cache4_read_f16", "fa_cache4_attend_f16", "fa_get_status", "fa_watchdog_selftest", "fa_version", "fa_dropout_rate",
     "fa_launch_plan",
-    "forward", "backward", "attention", "FlashAttentionFunction",
+    "forward", "backward", "attention", "FlashAttentionFunction", "cache4_empty",
+    "cache4_append", "cache4_read", "cache4_attend",
 ]
 
 
@@ -433,6 +435,91 @@ def fa_backward_scored_f16(Q, K, V, O, dO, LSE, dQ, dK, dV, scale: float, causal
                      scale, causal, workspace, window, softcap, slopes, documents, prefix, stream)
 
 
+def _cache4(codes, params, page_table, dtype, B, Hkv, d):
+    """(codes, params, page table pointers), (page, n_pages, max_pages)."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 5:
+        raise ValueError("codes must be a [pages, 2, K/V heads, page, d / 2] tensor")
+    n_pages, _, _, page, _ = (int(x) for x in codes.shape)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [B, pages per sequence] tensor")
+    max_pages = int(page_table.shape[1])
+    return ((_need("codes", codes, torch.uint8, (n_pages, 2, Hkv, page, d // 2)),
+             _need("params", params, dtype, (n_pages, 2, Hkv, page, 2)),
+             _need("page_table", page_table, torch.int32, (B, max_pages))),
+            (page, n_pages, max_pages))
+
+
+def _cache4_rows(name, dtype, K, V, codes, params, page_table, positions, counts, stream):
+    B, Hkv, n, d = _shape(K)
+    kv = (_need("K", K, dtype, (B, Hkv, n, d)), _need("V", V, dtype, (B, Hkv, n, d)))
+    ptrs, sizes = _cache4(codes, params, page_table, dtype, B, Hkv, d)
+    check(name, getattr(lib(), name)(
+        *kv, *ptrs, _need("positions", positions, torch.int32, (B,)),
+        _device_array("counts", counts, torch.int32, (B,)), B, Hkv, n, d, *sizes,
+        _stream(stream)))
+
+
+def _cache4_attend(name, dtype, Q, O, LSE, codes, params, page_table, lengths, max_len, scale,
+                   window_left, softcap, slopes, workspace, stream):
+    B, H, Nq, d = _shape(Q)
+    Hkv = int(codes.shape[2]) if codes.dim() == 5 else 0
+    qo = (_need("Q", Q, dtype, (B, H, Nq, d)), _need("O", O, dtype, (B, H, Nq, d)),
+          _need("LSE", LSE, torch.float32, (B, H, Nq)))
+    ptrs, (page, n_pages, max_pages) = _cache4(codes, params, page_table, dtype, B, Hkv, d)
+    ws, nbytes = (None, 0) if workspace is None else _ws(workspace)
+    check(name, getattr(lib(), name)(
+        *qo, *ptrs, _need("lengths", lengths, torch.int32, (B,)), B, H, Hkv, Nq, d, page, n_pages,
+        max_pages, int(max_len), float(scale), int(window_left),
+        0.0 if softcap is None else float(softcap),
+        _device_array("slopes", slopes, torch.float32, (H,)), ws, nbytes, _stream(stream)))
+
+
+@_on_one_device
+def fa_cache4_append(K, V, codes, params, page_table, positions, counts=None,
+                     stream=None) -> None:
+    """K, V (bf16 [B, Hkv, n, d]) into a 4-bit cache at positions[b] .. of sequence b."""
+    _cache4_rows("fa_cache4_append", torch.bfloat16, K, V, codes, params, page_table, positions,
+                 counts, stream)
+
+
+@_on_one_device
+def fa_cache4_append_f16(K, V, codes, params, page_table, positions, counts=None,
+                         stream=None) -> None:
+    _cache4_rows("fa_cache4_append_f16", torch.float16, K, V, codes, params, page_table,
+                 positions, counts, stream)
+
+
+@_on_one_device
+def fa_cache4_read(K, V, codes, params, page_table, positions, counts=None, stream=None) -> None:
+    """Rows of a 4-bit cache into K, V (bf16 [B, Hkv, n, d])."""
+    _cache4_rows("fa_cache4_read", torch.bfloat16, K, V, codes, params, page_table, positions,
+                 counts, stream)
+
+
+@_on_one_device
+def fa_cache4_read_f16(K, V, codes, params, page_table, positions, counts=None,
+                       stream=None) -> None:
+    _cache4_rows("fa_cache4_read_f16", torch.float16, K, V, codes, params, page_table, positions,
+                 counts, stream)
+
+
+@_on_one_device
+def fa_cache4_attend(Q, O, LSE, codes, params, page_table, lengths, max_len: int, scale: float,
+                     window_left: int = -1, softcap=None, slopes=None, workspace=None,
+                     stream=None) -> None:
+    """The last Nq tokens of each sequence over a 4-bit cache (bf16)."""
+    _cache4_attend("fa_cache4_attend", torch.bfloat16, Q, O, LSE, codes, params, page_table,
+                   lengths, max_len, scale, window_left, softcap, slopes, workspace, stream)
+
+
+@_on_one_device
+def fa_cache4_attend_f16(Q, O, LSE, codes, params, page_table, lengths, max_len: int,
+                         scale: float, window_left: int = -1, softcap=None, slopes=None,
+                         workspace=None, stream=None) -> None:
+    _cache4_attend("fa_cache4_attend_f16", torch.float16, Q, O, LSE, codes, params, page_table,
+                   lengths, max_len, scale, window_left, softcap, slopes, workspace, stream)
+
+
 @_on_one_device
 def fa_get_status(stream=None) -> int:
     """Synchronises the stream; returns the library status code (0 = ok, 4 = a
@@ -584,3 +671,62 @@ def attention(q, k, v, causal: bool = False, scale=None, window=None, block_mask
     ``prefix`` as for ``forward``; slopes are constants (no gradient)."""
     return FlashAttentionFunction.apply(q, k, v, causal, scale, window, block_mask, dropout,
                                         softcap, slopes, documents, prefix)
+
+
+# ---------------------------------------------------------------- 4-bit cache
+
+
+def _cache4_suffix(dtype) -> str:
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"the 4-bit cache serves bf16 and f16 models, not {dtype}")
+    return "" if dtype == torch.bfloat16 else "_f16"
+
+
+def cache4_empty(n_pages: int, kv_heads: int, page: int, d: int, dtype=torch.bfloat16,
+                 device="cuda"):
+    """(codes, params) of a cache of n_pages pages of ``page`` tokens (16, 32, 64, 128 or
+    256) for K and V of kv_heads heads; see fa_cache4_append in include/fa.h."""
+    _cache4_suffix(dtype)
+    if page not in (16, 32, 64, 128, 256):
+        raise ValueError(f"a page holds 16, 32, 64, 128 or 256 tokens, not {page}")
+    if d not in (64, 128):
+        raise ValueError(f"d must be 64 or 128, got {d}")
+    return (torch.empty(n_pages, 2, kv_heads, page, d // 2, dtype=torch.uint8, device=device),
+            torch.empty(n_pages, 2, kv_heads, page, 2, dtype=dtype, device=device))
+
+
+def cache4_append(codes, params, k, v, page_table, positions, counts=None) -> None:
+    """Puts k, v ([B, kv heads, n, d], bf16 or f16) into the cache: token t of sequence b at
+    position positions[b] + t, for t < counts[b] (all n without counts)."""
+    fn = fa_cache4_append_f16 if _cache4_suffix(k.dtype) else fa_cache4_append
+    fn(k, v, codes, params, page_table, positions, counts)
+
+
+def cache4_read(codes, params, page_table, positions, n: int, counts=None):
+    """(k, v), [B, kv heads, n, d], as the cache holds them at positions[b] .. positions[b] +
+    n - 1; zeros behind counts[b]."""
+    shape = (page_table.shape[0], codes.shape[2], n, 2 * codes.shape[4])
+    k = torch.empty(shape, dtype=params.dtype, device=codes.device)
+    v = torch.empty_like(k)
+    fn = fa_cache4_read_f16 if _cache4_suffix(params.dtype) else fa_cache4_read
+    fn(k, v, codes, params, page_table, positions, counts)
+    return k, v
+
+
+def cache4_attend(q, codes, params, page_table, lengths, scale=None, window_left: int = -1,
+                  softcap=None, slopes=None, max_len=None):
+    """(O, LSE) of the last tokens q ([B, H, n, d]; n = 1 when decoding) of sequences of
+    ``lengths`` tokens (int32 [B], these tokens included) over a 4-bit cache. Scores as for
+    ``forward``, causal. ``max_len``: a bound on the lengths known on the host (default: what
+    the page table has room for); a close one gives a better cut of the work."""
+    B, H, n, d = _shape(q)
+    room = int(page_table.shape[1]) * int(codes.shape[3])
+    max_len = room if max_len is None else min(int(max_len), room)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
+    nbytes = lib().fa_cache4_workspace_size(B, H, int(codes.shape[2]), n, d, max_len, window_left)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    fn = fa_cache4_attend_f16 if _cache4_suffix(q.dtype) else fa_cache4_attend
+    fn(q, o, lse, codes, params, page_table, lengths, max_len, _default_scale(d, scale),
+       window_left, softcap, slopes, ws)
+    return o, lse

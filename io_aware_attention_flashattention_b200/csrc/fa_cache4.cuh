@@ -1,0 +1,633 @@
+// fa_cache4.cuh -- a key/value cache held in 4 bits: appending rows, reading rows back,
+// and the attention of single tokens and short drafts over it.
+//
+// A row (one token's K or V of one head, d values) is held as d codes of 4 bits and a pair
+// (scale, zero) in the model's 16-bit type:
+//   zero = min x, scale = (max x - min x) / 15, code = round((x - zero) / scale),
+//   value = scale * code + zero.
+// Rows lie in pages of `page` tokens: codes [n_pages, 2 (K, V), Hkv, page, d/2] bytes, the
+// even channel of a pair in the low four bits; params [n_pages, 2, Hkv, page] words, the
+// scale in the low half. Token t of sequence b is slot t % page of page
+// table[b][t / page]. Pages hold whole groups of 16 tokens, so no group straddles two.
+#pragma once
+
+#include "fa_ptx.cuh"
+#include "fa_score.cuh"
+
+namespace fa {
+namespace cache4 {
+
+struct Layout {
+  uint8_t* codes;
+  uint32_t* params;
+  const int* table;  // [B, max_pages]
+  long long n_pages;
+  int max_pages;
+  int Hkv;
+  int page;   // tokens per page: a power of two from 16 to 256
+  int shift;  // its logarithm
+};
+
+// Index of the first row (slot 0) of a page's K (which = 0) or V (1) of one head.
+__host__ __device__ __forceinline__ long long page_row(long long id, int which, int hk, int Hkv,
+                                                       int shift) {
+  return ((id * 2 + which) * Hkv + hk) << shift;
+}
+
+// The page that holds token t of a sequence with this page table row; -1 if t lies outside
+// the table or its entry outside the cache.
+__host__ __device__ __forceinline__ long long page_of(const int* table_row, int max_pages,
+                                                      long long n_pages, int shift, long long t) {
+  if (t < 0) return -1;
+  const long long at = t >> shift;
+  if (at >= max_pages) return -1;
+  const long long id = table_row[at];
+  return id >= 0 && id < n_pages ? id : -1;
+}
+
+template <Elt E>
+__device__ __forceinline__ float2 scale_zero(uint32_t w) {
+  return unpack2<E>(w);
+}
+
+// ------------------------------------------------------------------ append
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Row (b, head, t) of K (blockIdx.y = 0) or V (1) by D / 8 neighbouring lanes, 8 channels
+// (one 16-byte load, one word of codes) each. Reads 2 D bytes and writes D / 2 + 4 per row:
+// bound by memory.
+template <int D, Elt E>
+__global__ void __launch_bounds__(256)
+    append_kernel(const uint16_t* __restrict__ K, const uint16_t* __restrict__ V, const Layout L,
+                  const int* __restrict__ positions, const int* __restrict__ counts, int n,
+                  long long rows) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int G = D / 8;  // lanes of a row
+  const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;
+  const int lane = threadIdx.x % G, which = blockIdx.y;
+  if (r >= rows) return;  // rows = B * Hkv * n; whole groups of lanes leave
+  const int t = static_cast<int>(r % n);
+  const long long bh = r / n;
+  const int hk = static_cast<int>(bh % L.Hkv), b = static_cast<int>(bh / L.Hkv);
+  if (counts != nullptr && t >= counts[b]) return;
+  const long long pos = static_cast<long long>(positions[b]) + t;
+  const long long id = page_of(L.table + static_cast<size_t>(b) * L.max_pages, L.max_pages,
+                               L.n_pages, L.shift, pos);
+  if (id < 0) {
+    if (lane == 0) atomicOr(&g_status, kStatusBadPage);
+    return;
+  }
+  const uint4 w = reinterpret_cast<const uint4*>((which ? V : K) + r * D)[lane];
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  float x[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2<E>(ws[k]);
+    x[2 * k] = f.x;
+    x[2 * k + 1] = f.y;
+  }
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    lo = min_nan(lo, x[k]);
+    hi = max_nan(hi, x[k]);
+  }
+  const unsigned group = G == 32 ? 0xffffffffu
+                                 : ((1u << G) - 1u) << ((threadIdx.x & 31) / G * G);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(group, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(group, hi, o));
+  }
+  // The step rounded to 16 bits is the step that codes are made for and values read with;
+  // the zero is one of the row's own values, so it needs no rounding. Each bound is divided
+  // by itself: their difference may pass the largest bf16.
+  constexpr float kFifteenth = 1.0f / 15.0f;
+  const uint32_t sz = pack2<E>(__fsub_rn(__fmul_rn(hi, kFifteenth), __fmul_rn(lo, kFifteenth)), lo);
+  const float scale = scale_zero<E>(sz).x;
+  uint32_t code = 0;
+  if (scale > 0.0f) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float c = fminf(fmaxf(rintf(__fdiv_rn(x[k] - lo, scale)), 0.0f), 15.0f);
+      code |= static_cast<uint32_t>(c) << (4 * k);
+    }
+  }
+  const long long row = page_row(id, which, hk, L.Hkv, L.shift) + (pos & (L.page - 1));
+  reinterpret_cast<uint32_t*>(L.codes + row * (D / 2))[lane] = code;
+  if (lane == 0) L.params[row] = sz;
+}
+
+// ------------------------------------------------------------------ read
+
+// The same rows back as 16-bit values [B, Hkv, n, D]; rows behind a count are zeros.
+template <int D, Elt E>
+__global__ void __launch_bounds__(256)
+    read_kernel(uint16_t* __restrict__ K, uint16_t* __restrict__ V, const Layout L,
+                const int* __restrict__ positions, const int* __restrict__ counts, int n,
+                long long rows) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int G = D / 8;
+  const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;
+  const int lane = threadIdx.x % G, which = blockIdx.y;
+  if (r >= rows) return;
+  const int t = static_cast<int>(r % n);
+  const long long bh = r / n;
+  const int hk = static_cast<int>(bh % L.Hkv), b = static_cast<int>(bh / L.Hkv);
+  uint4 out = make_uint4(0u, 0u, 0u, 0u);
+  if (counts == nullptr || t < counts[b]) {
+    const long long pos = static_cast<long long>(positions[b]) + t;
+    const long long id = page_of(L.table + static_cast<size_t>(b) * L.max_pages, L.max_pages,
+                                 L.n_pages, L.shift, pos);
+    if (id < 0) {
+      if (lane == 0) atomicOr(&g_status, kStatusBadPage);
+    } else {
+      const long long row = page_row(id, which, hk, L.Hkv, L.shift) + (pos & (L.page - 1));
+      const uint32_t code = reinterpret_cast<const uint32_t*>(L.codes + row * (D / 2))[lane];
+      const float2 sz = scale_zero<E>(L.params[row]);
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o[k] = pack2<E>(fmaf(sz.x, static_cast<float>((code >> (8 * k)) & 15u), sz.y),
+                        fmaf(sz.x, static_cast<float>((code >> (8 * k + 4)) & 15u), sz.y));
+      out = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  reinterpret_cast<uint4*>((which ? V : K) + r * D)[lane] = out;
+}
+
+// ------------------------------------------------------------------ attend
+//
+// One CTA of kWarps warps takes one K/V head of one sequence, up to 8 * NT query rows (the
+// group's heads times the draft's tokens) and a piece of the sequence; every warp takes
+// every kWarps-th group of 16 tokens of it and keeps its own running maximum, sum and
+// output, joined at the end over the warps and then (by combine_kernel) over the pieces.
+// Products on the tensor cores (mma.m16n8k16, fp32 accumulators) with tokens, then
+// channels, as the 16 rows, so that up to 8 query rows cost one product:
+//   S^T[16 tokens x 8 rows] = codes[16 x d] Q^T[d x 8]
+//   O^T[d x 8] += V codes^T[d x 16] P^T[16 x 8]
+// Codes go from global memory to registers in the order the products take them: a thread
+// holds whole words of 8 codes and any order of the summed index will do, as long as both
+// operands follow it. A code becomes a 16-bit float by a shift and one logical operation
+// (16 + code, the code placed in the mantissa of 16). With sum q = qs:
+//   s = scale_k * (sum q (16 + c)) + (zero_k - 16 scale_k) qs
+// and, with P' = P scale_v rounded to bf16 and codes brought to c - 8 (exact),
+//   o = sum P' (c - 8) + sum (P zero_v + 8 P').
+// P' is bf16 for both element types: scales times weights of long rows would fall below
+// f16's normal range. The reference maximum of a row moves only when a score passes it by
+// more than 2^8, as in the forward.
+// Bound by memory: d + 8 bytes per token and head (K and V).
+
+constexpr int kWarps = 4;
+constexpr int kGroup = 16;  // tokens per step of a warp
+
+struct AttendParams {
+  const uint16_t* Q;  // [B, H, Nq, D]
+  uint16_t* O;
+  float* LSE;  // [B, H, Nq]
+  const int* lengths;
+  float* part_o;   // [B * H * Nq][n_pieces][D], pieces > 1 only
+  float2* part_ml;  // [B * H * Nq][n_pieces] (maximum in log2 units, sum)
+  Layout L;
+  ScoreParams score;
+  int B, H, Nq;
+  int rows;      // query rows per K/V head: group * Nq
+  int row_tiles;  // CTAs they take
+  int n_pieces;
+  int piece;  // groups per piece, a multiple of kWarps
+  int wl;     // < 0: no window
+  float scale_log2;
+};
+
+__device__ __forceinline__ void mma_16n8k16_bf16(float (&c)[4], const uint32_t (&a)[4],
+                                                 uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16n8k16_f16(float (&c)[4], const uint32_t (&a)[4],
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The 8 x 8 matrix of 16-bit elements that a warp holds as an accumulator's half, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Nibbles j of both halves of a word as a pair of 16-bit floats 16 + code.
+template <Elt E, int j>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
+  constexpr int s = (E == Elt::BF16 ? 3 : 6) - 4 * j;  // to the mantissa bits that count units
+  const uint32_t m = s >= 0 ? w << (s >= 0 ? s : 0) : w >> (s < 0 ? -s : 0);
+  constexpr uint32_t mask = E == Elt::BF16 ? 0x00780078u : 0x03C003C0u;
+  constexpr uint32_t sixteen = E == Elt::BF16 ? 0x41804180u : 0x4C004C00u;
+  return (m & mask) | sixteen;
+}
+
+// The same less 24: code - 8, exactly, in bf16.
+template <int j>
+__device__ __forceinline__ uint32_t centred(uint32_t w) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(nibbles<Elt::BF16, j>(w)), "r"(0xC1C0C1C0u));
+  return r;
+}
+
+// What a warp holds of 16 tokens of one head: thread (g, t) = (lane / 4, lane % 4).
+template <int D>
+struct Piece {
+  uint32_t k[2][D / 32];  // rows g', g' + 8: channels t * D / 4 on
+  uint32_t v[4][D / 64];  // tokens t, 4 + t, 8 + t, 12 + t: channels g * D / 8 on
+  uint32_t kp[2], vp[2];  // (scale, zero) of tokens g', g' + 8
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&r)[N], const uint8_t* p) {
+  if constexpr (N == 4) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    r[0] = w.x; r[1] = w.y; r[2] = w.z; r[3] = w.w;
+  } else if constexpr (N == 2) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    r[0] = w.x; r[1] = w.y;
+  } else {
+    r[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_piece(Piece<D>& x, const Layout& L, long long id, int hk,
+                                           int slot, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const int own = (g >> 1) + (g & 1) * 4;  // the token of the product's row g
+  const long long kr = page_row(id, 0, hk, L.Hkv, L.shift) + slot;
+  const long long vr = page_row(id, 1, hk, L.Hkv, L.shift) + slot;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_words(x.k[h], L.codes + (kr + own + 8 * h) * (D / 2) + t * (D / 8));
+    x.kp[h] = __ldg(L.params + kr + own + 8 * h);
+    x.vp[h] = __ldg(L.params + vr + own + 8 * h);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    load_words(x.v[i], L.codes + (vr + 4 * i + t) * (D / 2) + g * (D / 16));
+}
+
+template <int D, Elt E, int NT>
+__global__ void __launch_bounds__(kWarps * 32)
+    attend_kernel(const AttendParams p) {
+  constexpr int R = 8 * NT;      // query rows of the CTA
+  constexpr int KS = D / 16;     // steps of the score product
+  constexpr int MT = D / 16;     // 16-channel blocks of the output
+  __shared__ float sm_o[kWarps][R][D + 4];
+  __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  long long at = blockIdx.x;
+  const int piece = static_cast<int>(at % p.n_pieces);
+  at /= p.n_pieces;
+  const int rt = static_cast<int>(at % p.row_tiles);
+  at /= p.row_tiles;
+  const int hk = static_cast<int>(at % p.L.Hkv), b = static_cast<int>(at / p.L.Hkv);
+  const int row0 = rt * R;
+  const int n_rows = min(R, p.rows - row0);
+  const int group = p.score.group;
+  // the row of [B, H, Nq] that row r of this K/V head is
+  auto out_row = [&](int r) -> long long {
+    return (static_cast<long long>(b) * p.H + hk * group + r / p.Nq) * p.Nq + r % p.Nq;
+  };
+
+  const long long room = static_cast<long long>(p.L.max_pages) * p.L.page;
+  int len = p.lengths[b];
+  if (len < 0) len = 0;
+  if (len > room) {
+    len = static_cast<int>(room);
+    if (threadIdx.x == 0) atomicOr(&g_status, kStatusBadPage);
+  }
+  const int pos0 = len - p.Nq;  // of the draft's first token
+  const int first = p.wl < 0 ? 0 : max(0, pos0 - p.wl);
+  const int g_lo = first / kGroup, g_hi = (len + kGroup - 1) / kGroup;
+  const int* table = p.L.table + static_cast<size_t>(b) * p.L.max_pages;
+
+  // this warp's groups: g_lo + piece * p.piece + warp, every kWarps-th of the piece, then the
+  // same of piece + n_pieces, ... (more than one only where a length passes the given bound)
+  int grp = g_lo + piece * p.piece + warp, in_piece = 0;
+  auto next = [&](int x, int& in) -> int {
+    in += kWarps;
+    x += kWarps;
+    if (in >= p.piece) {
+      in = 0;
+      x += (p.n_pieces - 1) * p.piece;
+    }
+    return x;
+  };
+
+  // the queries, as the score product's second operand, and the sums of their channels
+  uint32_t q[NT][KS][2];
+  float qs[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = row0 + nt * 8 + g;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (r < p.rows)
+        x = __ldg(reinterpret_cast<const uint4*>(p.Q + out_row(r) * D + t * (D / 4) + 8 * w));
+      const float2 f0 = unpack2<E>(x.x), f1 = unpack2<E>(x.y), f2 = unpack2<E>(x.z),
+                   f3 = unpack2<E>(x.w);
+      sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+      q[nt][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);      // channels 0, 4
+      q[nt][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);      // 1, 5
+      q[nt][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);  // 2, 6
+      q[nt][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    qs[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+    qs[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+  }
+  // this thread's rows of the products' results: 2t and 2t + 1 of each 8
+  int pos[NT][2];
+  float slope_neg[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = min(row0 + nt * 8 + 2 * t + e, p.rows - 1);
+      pos[nt][e] = pos0 + r % p.Nq;
+      slope_neg[nt][e] =
+          p.score.slopes ? -p.score.slopes[hk * group + r / p.Nq] * p.score.slope_mul : 0.0f;
+    }
+
+  const float c = p.scale_log2;
+  float m[NT][2], l[NT][2], z[NT][2], o[NT][MT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[nt][e] = -INFINITY;
+      l[nt][e] = z[nt][e] = 0.0f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.0f;
+  }
+
+  auto page_id = [&](int x) -> long long {
+    return x < g_hi ? page_of(table, p.L.max_pages, p.L.n_pages, p.L.shift,
+                              static_cast<long long>(x) * kGroup)
+                    : -1;
+  };
+  Piece<D> ahead;
+  long long id = page_id(grp);
+  load_piece(ahead, p.L, id < 0 ? 0 : id, hk, id < 0 ? 0 : (grp * kGroup) & (p.L.page - 1), lane);
+  while (grp < g_hi) {
+    const Piece<D> x = ahead;
+    const bool bad = id < 0;
+    const int k0 = grp * kGroup;
+    grp = next(grp, in_piece);
+    id = page_id(grp);
+    if (grp < g_hi)
+      load_piece(ahead, p.L, id < 0 ? 0 : id, hk, id < 0 ? 0 : (grp * kGroup) & (p.L.page - 1), lane);
+    if (bad) {  // tokens without a page are not there
+      if (lane == 0) atomicOr(&g_status, kStatusBadPage);
+      continue;
+    }
+    const int own = (g >> 1) + (g & 1) * 4;
+    float2 ksz[2], vsz[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      ksz[h] = scale_zero<E>(x.kp[h]);
+      vsz[h] = scale_zero<E>(x.vp[h]);
+      ksz[h].y = fmaf(-16.0f, ksz[h].x, ksz[h].y);
+    }
+    // scores: (token own + 8h, row 2t + e) is s[nt][2h + e]
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      const uint32_t a0[4] = {nibbles<E, 0>(x.k[0][w]), nibbles<E, 0>(x.k[1][w]),
+                              nibbles<E, 1>(x.k[0][w]), nibbles<E, 1>(x.k[1][w])};
+      const uint32_t a1[4] = {nibbles<E, 2>(x.k[0][w]), nibbles<E, 2>(x.k[1][w]),
+                              nibbles<E, 3>(x.k[0][w]), nibbles<E, 3>(x.k[1][w])};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (E == Elt::BF16) {
+          mma_16n8k16_bf16(s[nt], a0, q[nt][2 * w][0], q[nt][2 * w][1]);
+          mma_16n8k16_bf16(s[nt], a1, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+        } else {
+          mma_16n8k16_f16(s[nt], a0, q[nt][2 * w][0], q[nt][2 * w][1]);
+          mma_16n8k16_f16(s[nt], a1, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+        }
+      }
+    }
+    uint32_t u[4 * NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        u[4 * nt + e] =
+            __float_as_uint(fmaf(ksz[e >> 1].x, s[nt][e], ksz[e >> 1].y * qs[nt][e & 1]));
+    if (p.score.cap_in2 != 0.0f) tanh_scores(u, p.score);
+    // rows' keys are [pos - wl, pos]: tests only where the 16 tokens cross an edge
+    const bool edge = k0 + kGroup - 1 > pos0 || (p.wl >= 0 && k0 < len - 1 - p.wl);
+    bool up = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = k0 + own + 8 * (e >> 1);
+        float y = __uint_as_float(u[4 * nt + e]);
+        if (p.score.slopes)
+          y = fmaf(slope_neg[nt][e & 1], static_cast<float>(pos[nt][e & 1] - key), y);
+        if (edge && (key > pos[nt][e & 1] || (p.wl >= 0 && key < pos[nt][e & 1] - p.wl)))
+          y = -INFINITY;
+        s[nt][e] = y;
+        up = up || y * c > m[nt][e & 1] + 8.0f;
+      }
+    if (edge) {
+      // a token that no row sees has weight 0, whatever its slot holds
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = k0 + own + 8 * h;
+        if (key >= len || (p.wl >= 0 && key < pos0 - p.wl)) vsz[h] = make_float2(0.0f, 0.0f);
+      }
+    }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(s[nt][e], s[nt][2 + e]) * c;
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const float now = fmaxf(m[nt][e], top);
+          alpha[e] = m[nt][e] == -INFINITY ? 0.0f : ex2_approx(m[nt][e] - now);
+          m[nt][e] = now;
+          l[nt][e] *= alpha[e];
+          z[nt][e] *= alpha[e];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
+      }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float base = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
+        w[e] = ex2_approx(fmaf(s[nt][e], c, -base));
+        l[nt][e & 1] += w[e];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t pk = pack_bf16x2(w[2 * h] * vsz[h].x, w[2 * h + 1] * vsz[h].x);
+        const float2 back = unpack2<Elt::BF16>(pk);
+        z[nt][0] += fmaf(w[2 * h], vsz[h].y, 8.0f * back.x);
+        z[nt][1] += fmaf(w[2 * h + 1], vsz[h].y, 8.0f * back.y);
+        pb[nt][h] = transpose8(pk);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) {
+      const uint32_t lo0 = __byte_perm(x.v[0][w], x.v[1][w], 0x5410);
+      const uint32_t lo1 = __byte_perm(x.v[2][w], x.v[3][w], 0x5410);
+      const uint32_t hi0 = __byte_perm(x.v[0][w], x.v[1][w], 0x7632);
+      const uint32_t hi1 = __byte_perm(x.v[2][w], x.v[3][w], 0x7632);
+      const uint32_t a[4][4] = {{centred<0>(lo0), centred<1>(lo0), centred<0>(lo1), centred<1>(lo1)},
+                                {centred<2>(lo0), centred<3>(lo0), centred<2>(lo1), centred<3>(lo1)},
+                                {centred<0>(hi0), centred<1>(hi0), centred<0>(hi1), centred<1>(hi1)},
+                                {centred<2>(hi0), centred<3>(hi0), centred<2>(hi1), centred<3>(hi1)}};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16n8k16_bf16(o[nt][4 * w + i], a[i], pb[nt][0], pb[nt][1]);
+    }
+  }
+
+  // this warp's rows into shared memory: row 2t + e, channels g * D / 8 + 8w + 2i + (0, 1)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+        z[nt][e] += __shfl_xor_sync(0xffffffffu, z[nt][e], d);
+      }
+      const int r = nt * 8 + 2 * t + e;
+      if (g == 0) {
+        sm_m[warp][r] = m[nt][e];
+        sm_l[warp][r] = l[nt][e];
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        *reinterpret_cast<float2*>(&sm_o[warp][r][g * (D / 8) + 2 * mt]) =
+            make_float2(o[nt][mt][e] + z[nt][e], o[nt][mt][2 + e] + z[nt][e]);
+    }
+  __syncthreads();
+  // the warps' rows joined: D / 4 threads a row
+  constexpr int T = D / 4;
+  for (int r = threadIdx.x / T; r < n_rows; r += kWarps * 32 / T) {
+    const int ch = (threadIdx.x % T) * 4;
+    float top = sm_m[0][r];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][r]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ex2_approx(sm_m[w][r] - base);
+      const float4 v = *reinterpret_cast<const float4*>(&sm_o[w][r][ch]);
+      sum = fmaf(f, sm_l[w][r], sum);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    const long long row = out_row(row0 + r);
+    if (p.n_pieces > 1) {
+      const long long slot = row * p.n_pieces + piece;
+      if (ch == 0) p.part_ml[slot] = make_float2(top, sum);
+      if (sum > 0.0f || sum != sum) *reinterpret_cast<float4*>(p.part_o + slot * D + ch) = acc;
+    } else {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      *reinterpret_cast<uint2*>(p.O + row * D + ch) =
+          make_uint2(pack2<E>(acc.x * inv, acc.y * inv), pack2<E>(acc.z * inv, acc.w * inv));
+      if (ch == 0)
+        p.LSE[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    }
+  }
+}
+
+// A row's pieces joined, by one warp a row: each lane D / 32 channels.
+template <int D, Elt E>
+__global__ void __launch_bounds__(128)
+    combine_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
+                   uint16_t* __restrict__ O, float* __restrict__ LSE, long long rows,
+                   int n_pieces) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int C = D / 32;
+  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const float2* ml = part_ml + row * n_pieces;
+  float top = -INFINITY;
+  for (int k = lane; k < n_pieces; k += 32) top = fmaxf(top, ml[k].x);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f, acc[C];
+#pragma unroll
+  for (int k = 0; k < C; ++k) acc[k] = 0.0f;
+  for (int k = 0; k < n_pieces; ++k) {
+    const float2 w = ml[k];
+    if (w.y == 0.0f) continue;  // a piece without keys left its output unwritten
+    const float f = ex2_approx(w.x - base);
+    sum = fmaf(f, w.y, sum);
+    const float* v = part_o + (row * n_pieces + k) * D + lane * C;
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint32_t* out = reinterpret_cast<uint32_t*>(O + row * D + lane * C);
+#pragma unroll
+  for (int i = 0; i < C / 2; ++i) out[i] = pack2<E>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (lane == 0) LSE[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+}
+
+}  // namespace cache4
+}  // namespace fa

@@ -24,6 +24,7 @@
 #include "fa_fwd_sm100.cuh"
 #include "fa_bwd_sm100.cuh"
 #include "fa_simt_f32.cuh"
+#include "fa_cache4.cuh"
 
 namespace fa {
 namespace {
@@ -1076,6 +1077,167 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
   return dq_convert_impl<E>(dQ, B, H, N, d, scale, workspace, workspace_bytes, stream);
 }
 
+// ---------------------------------------------------------------- 4-bit cache
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+fa_status make_layout(void* codes, void* params, const int32_t* table, int Hkv, int d, int page,
+                      int64_t n_pages, int max_pages, cache4::Layout* L) {
+  if (Hkv < 1 || n_pages < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (page < 16 || page > 256 || (page & (page - 1)) != 0) return FA_ERR_UNSUPPORTED;
+  // tokens and rows: a sequence's positions stay below 2^31, a cache's rows below 2^40
+  if (static_cast<long long>(max_pages) * page >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (n_pages > (1ll << 30) || Hkv > (1 << 16)) return FA_ERR_UNSUPPORTED;
+  if (codes == nullptr || params == nullptr || table == nullptr) return FA_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(params) || !aligned4(table)) return FA_ERR_INVALID_ARG;
+  L->codes = static_cast<uint8_t*>(codes);
+  L->params = static_cast<uint32_t*>(params);
+  L->table = table;
+  L->n_pages = n_pages;
+  L->max_pages = max_pages;
+  L->Hkv = Hkv;
+  L->page = page;
+  L->shift = 0;
+  while ((1 << L->shift) < page) ++L->shift;
+  return FA_OK;
+}
+
+// Append (kAppend: K, V are read) and read back (K, V are written).
+template <Elt E, bool kAppend>
+fa_status cache4_rows_impl(const void* K, const void* V, void* codes, void* params,
+                           const int32_t* table, const int32_t* positions, const int32_t* counts,
+                           int B, int Hkv, int n, int d, int page, int64_t n_pages, int max_pages,
+                           fa_stream_t stream) {
+  if (B < 1 || n < 0) return FA_ERR_INVALID_ARG;
+  cache4::Layout L;
+  fa_status st = make_layout(codes, params, table, Hkv, d, page, n_pages, max_pages, &L);
+  if (st != FA_OK) return st;
+  const long long rows = static_cast<long long>(B) * Hkv * n;
+  if (rows >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (n == 0) return FA_OK;
+  if ((st = check_ptrs({K, V})) != FA_OK) return st;
+  if (positions == nullptr || !aligned4(positions) || !aligned4(counts)) return FA_ERR_INVALID_ARG;
+  if ((st = prepare_device()) != FA_OK) return st;
+  const dim3 grid(static_cast<unsigned>((rows * (d / 8) + 255) / 256), 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if constexpr (kAppend) {
+    const auto* k = static_cast<const uint16_t*>(K);
+    const auto* v = static_cast<const uint16_t*>(V);
+    if (d == 64)
+      return launch(cache4::append_kernel<64, E>, grid, 256, 0, s, k, v, L, positions, counts, n, rows);
+    return launch(cache4::append_kernel<128, E>, grid, 256, 0, s, k, v, L, positions, counts, n, rows);
+  } else {
+    auto* k = static_cast<uint16_t*>(const_cast<void*>(K));
+    auto* v = static_cast<uint16_t*>(const_cast<void*>(V));
+    if (d == 64)
+      return launch(cache4::read_kernel<64, E>, grid, 256, 0, s, k, v, L, positions, counts, n, rows);
+    return launch(cache4::read_kernel<128, E>, grid, 256, 0, s, k, v, L, positions, counts, n, rows);
+  }
+}
+
+// How an attend call is cut: query rows per CTA (8 or 16), pieces of a sequence and groups of
+// 16 tokens per piece, from the bound on the lengths that the caller gives.
+struct AttendPlan {
+  int rows, nt, row_tiles, piece, n_pieces;
+};
+
+constexpr long long kAttendCtas = 148 * 8;  // CTAs that a call is cut into, if it is long enough
+constexpr int kMinPiece = 2 * cache4::kWarps;  // groups: two per warp
+
+AttendPlan attend_plan(int B, int H, int Hkv, int Nq, int max_len, int window_left) {
+  AttendPlan a;
+  a.rows = H / Hkv * Nq;
+  a.nt = a.rows <= 8 ? 1 : 2;
+  a.row_tiles = (a.rows + 8 * a.nt - 1) / (8 * a.nt);
+  long long span = std::max(max_len, 1);
+  if (window_left >= 0) span = std::min<long long>(span, static_cast<long long>(window_left) + Nq + 15);
+  const long long groups = (span + cache4::kGroup - 1) / cache4::kGroup;
+  const long long heads = static_cast<long long>(B) * Hkv * a.row_tiles;
+  const long long want = std::max<long long>(1, (kAttendCtas + heads - 1) / heads);
+  long long piece = std::max<long long>((groups + want - 1) / want, kMinPiece);
+  piece = (piece + cache4::kWarps - 1) / cache4::kWarps * cache4::kWarps;
+  a.piece = static_cast<int>(piece);
+  a.n_pieces = static_cast<int>((groups + piece - 1) / piece);
+  return a;
+}
+
+size_t attend_ws_bytes(const AttendPlan& a, int B, int H, int Nq, int d) {
+  if (a.n_pieces <= 1) return 0;
+  const size_t slots = static_cast<size_t>(B) * H * Nq * a.n_pieces;
+  return round256(slots * d * sizeof(float)) + round256(slots * sizeof(float2));
+}
+
+fa_status check_attend(int B, int H, int Hkv, int Nq, int d, int max_len) {
+  if (B < 1 || H < 1 || Hkv < 1 || Nq < 0 || max_len < 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  // row indices and grids stay below 2^31, with up to kAttendCtas pieces a row
+  if (static_cast<long long>(B) * H >= (1ll << 31) || Nq > (1 << 24) ||
+      static_cast<long long>(B) * H * std::max(Nq, 1) >= (1ll << 31) / kAttendCtas)
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+template <Elt E>
+fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* codes,
+                             const void* params, const int32_t* table, const int32_t* lengths,
+                             int B, int H, int Hkv, int Nq, int d, int page, int64_t n_pages,
+                             int max_pages, int max_len, float scale, int window_left,
+                             float softcap, const float* slopes, void* workspace,
+                             size_t workspace_bytes, fa_stream_t stream) {
+  fa_status st = check_attend(B, H, Hkv, Nq, d, max_len);
+  if (st != FA_OK) return st;
+  if (!(std::isfinite(scale) && scale > 0.0f)) return FA_ERR_INVALID_ARG;
+  cache4::AttendParams p;
+  if ((st = make_layout(const_cast<void*>(codes), const_cast<void*>(params), table, Hkv, d, page,
+                        n_pages, max_pages, &p.L)) != FA_OK)
+    return st;
+  if ((st = make_score(B, H, Hkv, scale, softcap, slopes, nullptr, 1, nullptr, &p.score)) != FA_OK)
+    return st;
+  if (Nq == 0) return FA_OK;
+  if ((st = check_ptrs({Q, O, LSE})) != FA_OK) return st;
+  if (lengths == nullptr || !aligned4(lengths)) return FA_ERR_INVALID_ARG;
+  max_len = static_cast<int>(std::min<long long>(max_len, static_cast<long long>(max_pages) * page));
+  const AttendPlan a = attend_plan(B, H, Hkv, Nq, max_len, window_left);
+  if (workspace_bytes < attend_ws_bytes(a, B, H, Nq, d)) return FA_ERR_INVALID_ARG;
+  if (a.n_pieces > 1 && (workspace == nullptr || !aligned16(workspace))) return FA_ERR_INVALID_ARG;
+  if ((st = prepare_device()) != FA_OK) return st;
+  p.Q = static_cast<const uint16_t*>(Q);
+  p.O = static_cast<uint16_t*>(O);
+  p.LSE = LSE;
+  p.lengths = lengths;
+  const long long rows = static_cast<long long>(B) * H * Nq;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(
+      static_cast<char*>(workspace) +
+      (a.n_pieces > 1 ? round256(static_cast<size_t>(rows) * a.n_pieces * d * sizeof(float)) : 0));
+  p.B = B;
+  p.H = H;
+  p.Nq = Nq;
+  p.rows = a.rows;
+  p.row_tiles = a.row_tiles;
+  p.n_pieces = a.n_pieces;
+  p.piece = a.piece;
+  p.wl = window_left < 0 ? -1 : window_left;
+  p.scale_log2 = score_log2(scale, softcap);
+  const unsigned grid = static_cast<unsigned>(static_cast<long long>(B) * Hkv * a.row_tiles * a.n_pieces);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  constexpr int T = cache4::kWarps * 32;
+  if (d == 64)
+    st = a.nt == 1 ? launch(cache4::attend_kernel<64, E, 1>, grid, T, 0, s, p)
+                   : launch(cache4::attend_kernel<64, E, 2>, grid, T, 0, s, p);
+  else
+    st = a.nt == 1 ? launch(cache4::attend_kernel<128, E, 1>, grid, T, 0, s, p)
+                   : launch(cache4::attend_kernel<128, E, 2>, grid, T, 0, s, p);
+  if (st != FA_OK || a.n_pieces == 1) return st;
+  const unsigned blocks = static_cast<unsigned>((rows + 3) / 4);
+  if (d == 64)
+    return launch(cache4::combine_kernel<64, E>, blocks, 128, 0, s, p.part_o, p.part_ml, p.O, LSE,
+                  rows, a.n_pieces);
+  return launch(cache4::combine_kernel<128, E>, blocks, 128, 0, s, p.part_o, p.part_ml, p.O, LSE,
+                rows, a.n_pieces);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1089,6 +1251,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_UNSUPPORTED: return "unsupported configuration or device";
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_TIMEOUT: return "kernel watchdog timeout";
+    case FA_ERR_BAD_PAGE: return "cache position without a page";
   }
   return "unknown status";
 }
@@ -1155,7 +1318,8 @@ fa_status fa_get_status(fa_stream_t stream) {
   if (cudaMemcpyFromSymbol(&v, g_status, sizeof(v)) != cudaSuccess) return FA_ERR_CUDA;
   if (v != 0 && cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess)
     return FA_ERR_CUDA;
-  return (v & kStatusTimeout) ? FA_ERR_TIMEOUT : FA_OK;
+  if (v & kStatusTimeout) return FA_ERR_TIMEOUT;
+  return (v & kStatusBadPage) ? FA_ERR_BAD_PAGE : FA_OK;
 }
 
 fa_status fa_watchdog_selftest(int timeout_ms, fa_stream_t stream) {
@@ -1400,6 +1564,78 @@ fa_status fa_backward_scored_f16(const void* Q, const void* K, const void* V, co
                                         causal, window_left, window_right, softcap, slopes,
                                         documents, n_docs, prefix, workspace, workspace_bytes,
                                         stream);
+}
+
+fa_status fa_cache4_append(const void* K, const void* V, void* codes, void* params,
+                          const int32_t* page_table, const int32_t* positions,
+                          const int32_t* counts, int B, int Hkv, int n, int d, int page,
+                          int64_t n_pages, int max_pages, fa_stream_t stream) {
+  return cache4_rows_impl<Elt::BF16, true>(K, V, codes, params, page_table, positions, counts, B, Hkv,
+                                          n, d, page, n_pages, max_pages, stream);
+}
+
+fa_status fa_cache4_read(void* K, void* V, const void* codes, const void* params,
+                        const int32_t* page_table, const int32_t* positions,
+                        const int32_t* counts, int B, int Hkv, int n, int d, int page,
+                        int64_t n_pages, int max_pages, fa_stream_t stream) {
+  return cache4_rows_impl<Elt::BF16, false>(K, V, const_cast<void*>(codes), const_cast<void*>(params),
+                                           page_table, positions, counts, B, Hkv, n, d, page,
+                                           n_pages, max_pages, stream);
+}
+
+fa_status fa_cache4_attend(const void* Q, void* O, float* LSE, const void* codes,
+                          const void* params, const int32_t* page_table, const int32_t* lengths,
+                          int B, int H, int Hkv, int Nq, int d, int page, int64_t n_pages,
+                          int max_pages, int max_len, float scale, int window_left,
+                          float softcap, const float* slopes, void* workspace,
+                          size_t workspace_bytes, fa_stream_t stream) {
+  return cache4_attend_impl<Elt::BF16>(Q, O, LSE, codes, params, page_table, lengths, B, H, Hkv, Nq,
+                                      d, page, n_pages, max_pages, max_len, scale, window_left,
+                                      softcap, slopes, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_cache4_append_f16(const void* K, const void* V, void* codes, void* params,
+                          const int32_t* page_table, const int32_t* positions,
+                          const int32_t* counts, int B, int Hkv, int n, int d, int page,
+                          int64_t n_pages, int max_pages, fa_stream_t stream) {
+  return cache4_rows_impl<Elt::F16, true>(K, V, codes, params, page_table, positions, counts, B, Hkv,
+                                          n, d, page, n_pages, max_pages, stream);
+}
+
+fa_status fa_cache4_read_f16(void* K, void* V, const void* codes, const void* params,
+                        const int32_t* page_table, const int32_t* positions,
+                        const int32_t* counts, int B, int Hkv, int n, int d, int page,
+                        int64_t n_pages, int max_pages, fa_stream_t stream) {
+  return cache4_rows_impl<Elt::F16, false>(K, V, const_cast<void*>(codes), const_cast<void*>(params),
+                                           page_table, positions, counts, B, Hkv, n, d, page,
+                                           n_pages, max_pages, stream);
+}
+
+fa_status fa_cache4_attend_f16(const void* Q, void* O, float* LSE, const void* codes,
+                          const void* params, const int32_t* page_table, const int32_t* lengths,
+                          int B, int H, int Hkv, int Nq, int d, int page, int64_t n_pages,
+                          int max_pages, int max_len, float scale, int window_left,
+                          float softcap, const float* slopes, void* workspace,
+                          size_t workspace_bytes, fa_stream_t stream) {
+  return cache4_attend_impl<Elt::F16>(Q, O, LSE, codes, params, page_table, lengths, B, H, Hkv, Nq,
+                                      d, page, n_pages, max_pages, max_len, scale, window_left,
+                                      softcap, slopes, workspace, workspace_bytes, stream);
+}
+
+size_t fa_cache4_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int window_left) {
+  if (check_attend(B, H, Hkv, Nq, d, max_len) != FA_OK || Nq == 0) return 0;
+  return attend_ws_bytes(attend_plan(B, H, Hkv, Nq, max_len, window_left), B, H, Nq, d);
+}
+
+int64_t fa_cache4_row(const int32_t* page_table_row, int max_pages, int64_t n_pages, int Hkv,
+                      int page, int which, int head, int64_t token) {
+  if (page_table_row == nullptr || max_pages < 1 || Hkv < 1 || page < 16 || page > 256 ||
+      (page & (page - 1)) != 0 || (which != 0 && which != 1) || head < 0 || head >= Hkv)
+    return -1;
+  int shift = 0;
+  while ((1 << shift) < page) ++shift;
+  const long long id = cache4::page_of(page_table_row, max_pages, n_pages, shift, token);
+  return id < 0 ? -1 : cache4::page_row(id, which, head, Hkv, shift) + (token & (page - 1));
 }
 
 fa_status fa_forward_f32(const float* Q, const float* K, const float* V, float* O, float* LSE,

@@ -11,7 +11,7 @@
 namespace fa {
 
 // Error bits recorded in the device status word.
-enum : unsigned { kStatusTimeout = 1u };
+enum : unsigned { kStatusTimeout = 1u, kStatusBadPage = 2u };
 
 __device__ unsigned int g_status;  // per-GPU status word, read by fa_get_status()
 
