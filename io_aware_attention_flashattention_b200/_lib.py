@@ -87,6 +87,8 @@ class FAError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library. Raises if libfa_b200.so has not been built."""
     global _handle
+    if _handle is not None:
+        return _handle
     with _lock:
         if _handle is None:
             if not os.path.exists(LIB):
@@ -94,6 +96,7 @@ def lib() -> ctypes.CDLL:
                     f"{LIB} is missing: build it with "
                     "`python -m io_aware_attention_flashattention_b200.build`")
             h = ctypes.CDLL(LIB)
+            # (_handle is set only once every signature is)
             for name, (res, args) in SIGNATURES.items():
                 fn = getattr(h, name)
                 fn.restype = res

@@ -55,6 +55,22 @@ def _one_device(*args):
 def _on_one_device(fn):
     @functools.wraps(fn)
     def call(*args, **kwargs):
+        # The common case, everything on the current GPU, without a context to enter.
+        index = -1
+        for a in (*args, *kwargs.values()):
+            if isinstance(a, torch.Tensor):
+                i = a.get_device()  # -1 on the CPU
+            elif isinstance(a, torch.cuda.Stream):
+                i = a.device.index
+            else:
+                continue
+            if i != index and i >= 0:
+                if index >= 0:
+                    break
+                index = i
+        else:
+            if index < 0 or index == torch.cuda.current_device():
+                return fn(*args, **kwargs)
         with _one_device(*args, *kwargs.values()):
             return fn(*args, **kwargs)
     return call
@@ -62,17 +78,20 @@ def _on_one_device(fn):
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(getattr(stream, "cuda_stream", stream))
 
 
 def _shape(t: torch.Tensor):
     if t.dim() != 4:
         raise ValueError(f"expected a [B, H, N, d] tensor, got shape {tuple(t.shape)}")
-    return tuple(int(x) for x in t.shape)
+    return tuple(t.shape)
 
 
 def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape) -> int:
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:

@@ -50,122 +50,182 @@ __device__ __forceinline__ float2 scale_zero(uint32_t w) {
   return unpack2<E>(w);
 }
 
-// ------------------------------------------------------------------ append
+// Division of numbers below 2^31 by a number the host knows, as one product and a shift
+// (Granlund and Montgomery, "Division by invariant integers using multiplication", 1994):
+// with l = ceil(log2 n) and m = ceil(2^(31 + l) / n), x / n = x m >> (31 + l).
+struct Divisor {
+  uint32_t n, m;
+  int s;
+  __device__ __forceinline__ uint32_t quotient(uint32_t x) const {
+    return static_cast<uint32_t>((static_cast<unsigned long long>(x) * m) >> s);
+  }
+};
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// ------------------------------------------------------------------ append and read
+//
+// A row by D / 16 neighbouring lanes, 16 channels (32 bytes, 8 bytes of codes) each. The
+// kernels move 2 D + D / 2 + 4 bytes per row and are bound by memory as long as a thread
+// spends few enough instructions on its 16 channels: row indices by products instead of
+// divisions, the quotient by a reciprocal (see quantise), codes to floats by the mantissa.
+// B16 Hkv8 n2048 ragged d128 (260 MB both ways) with IEEE divisions for each: 95 us for
+// the append and 58 us for the read.
+
+struct RowsParams {
+  uint16_t* K;  // read by the append, written by the read
+  uint16_t* V;
+  Layout L;
+  const int* positions;
+  const int* counts;  // or null
+  Divisor n, hkv;
+  uint32_t rows;  // B * Hkv * n
+};
+
+// What a thread's row is: its batch entry's token t lies in `row` of the cache (-1: nowhere).
+template <int D>
+struct RowAt {
+  uint32_t r;
+  int lane, which;
+  bool counted;
+  long long row;
+};
+
+template <int D>
+__device__ __forceinline__ RowAt<D> row_at(const RowsParams& p) {
+  constexpr int G = D / 16;  // lanes of a row
+  RowAt<D> a;
+  a.r = blockIdx.x * (256u / G) + threadIdx.x / G;
+  a.lane = threadIdx.x % G;
+  a.which = blockIdx.y;
+  a.row = -1;
+  a.counted = false;
+  if (a.r >= p.rows) return a;
+  const uint32_t bh = p.n.quotient(a.r), b = p.hkv.quotient(bh);
+  const int t = static_cast<int>(a.r - bh * p.n.n), hk = static_cast<int>(bh - b * p.hkv.n);
+  a.counted = p.counts == nullptr || t < p.counts[b];
+  if (!a.counted) return a;
+  const long long pos = static_cast<long long>(p.positions[b]) + t;
+  const long long id = page_of(p.L.table + static_cast<size_t>(b) * p.L.max_pages, p.L.max_pages,
+                               p.L.n_pages, p.L.shift, pos);
+  if (id < 0) {
+    if (a.lane == 0) atomicOr(&g_status, kStatusBadPage);
+    return a;
+  }
+  a.row = page_row(id, a.which, hk, p.L.Hkv, p.L.shift) + (pos & (p.L.page - 1));
+  return a;
+}
+
+template <Elt E>
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (E == Elt::BF16)
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+
+// code = round((x - lo) / scale), halves to even, of the quotient rounded to 32 bits. The
+// product with the reciprocal lies within 3 roundings (3e-6 at 15) of that quotient, so it
+// rounds to the same code unless it comes within 1e-5 of a half: then, and where the scale
+// is below the type's normal numbers (codes may pass 15) or x - lo passes 32 bits, the
+// quotient itself is formed. Adding 1.5 * 2^23 rounds and leaves the code in the low bits.
+template <Elt E>
+__device__ __forceinline__ uint2 quantise(const float (&x)[16], float lo, float hi, float scale) {
+  constexpr float kMagic = 12582912.0f;
+  constexpr float kNormal = E == Elt::BF16 ? 1e-36f : 6.2e-5f;
+  const float inv = __frcp_rn(scale);
+  float worst = 0.0f;
+  uint32_t code[2] = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float d = x[k] - lo;
+    const float y = fmaf(d, inv, kMagic);
+    worst = fmaxf(worst, fabsf(fmaf(d, inv, -(y - kMagic))));
+    code[k / 8] += (__float_as_uint(y) & 15u) << (4 * (k % 8));
+  }
+  if (!(worst < 0.49999f) || !(scale >= kNormal) || !(hi - lo < 3.0e38f)) {
+    code[0] = code[1] = 0u;
+    if (scale > 0.0f) {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float v = h ? x[8 + k] : x[k];
+          const float c = fminf(fmaxf(rintf(__fdiv_rn(v - lo, scale)), 0.0f), 15.0f);
+          code[h] |= static_cast<uint32_t>(c) << (4 * k);
+        }
+    }
+  }
+  return make_uint2(code[0], code[1]);
 }
 
-// Row (b, head, t) of K (blockIdx.y = 0) or V (1) by D / 8 neighbouring lanes, 8 channels
-// (one 16-byte load, one word of codes) each. Reads 2 D bytes and writes D / 2 + 4 per row:
-// bound by memory.
 template <int D, Elt E>
-__global__ void __launch_bounds__(256)
-    append_kernel(const uint16_t* __restrict__ K, const uint16_t* __restrict__ V, const Layout L,
-                  const int* __restrict__ positions, const int* __restrict__ counts, int n,
-                  long long rows) {
+__global__ void __launch_bounds__(256) append_kernel(const RowsParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int G = D / 8;  // lanes of a row
-  const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;
-  const int lane = threadIdx.x % G, which = blockIdx.y;
-  if (r >= rows) return;  // rows = B * Hkv * n; whole groups of lanes leave
-  const int t = static_cast<int>(r % n);
-  const long long bh = r / n;
-  const int hk = static_cast<int>(bh % L.Hkv), b = static_cast<int>(bh / L.Hkv);
-  if (counts != nullptr && t >= counts[b]) return;
-  const long long pos = static_cast<long long>(positions[b]) + t;
-  const long long id = page_of(L.table + static_cast<size_t>(b) * L.max_pages, L.max_pages,
-                               L.n_pages, L.shift, pos);
-  if (id < 0) {
-    if (lane == 0) atomicOr(&g_status, kStatusBadPage);
-    return;
-  }
-  const uint4 w = reinterpret_cast<const uint4*>((which ? V : K) + r * D)[lane];
-  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-  float x[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 f = unpack2<E>(ws[k]);
-    x[2 * k] = f.x;
-    x[2 * k + 1] = f.y;
-  }
-  float lo = x[0], hi = x[0];
+  constexpr int G = D / 16;
+  const RowAt<D> a = row_at<D>(p);
+  if (a.row < 0) return;  // all lanes of a row alike
+  const uint4* src = reinterpret_cast<const uint4*>((a.which ? p.V : p.K) +
+                                                    static_cast<size_t>(a.r) * D) + 2 * a.lane;
+  const uint4 w0 = src[0], w1 = src[1];
+  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  // the least x and the least -x (NaN wins), of pairs, then of both halves as one pair
+  uint32_t lows = w[0], highs = w[0] ^ 0x80008000u;
 #pragma unroll
   for (int k = 1; k < 8; ++k) {
-    lo = min_nan(lo, x[k]);
-    hi = max_nan(hi, x[k]);
+    lows = min2_nan<E>(lows, w[k]);
+    highs = min2_nan<E>(highs, w[k] ^ 0x80008000u);
   }
-  const unsigned group = G == 32 ? 0xffffffffu
-                                 : ((1u << G) - 1u) << ((threadIdx.x & 31) / G * G);
+  uint32_t both = min2_nan<E>(__byte_perm(lows, highs, 0x5410), __byte_perm(lows, highs, 0x7632));
+  const unsigned group = ((1u << G) - 1u) << ((threadIdx.x & 31) / G * G);
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(group, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(group, hi, o));
-  }
+  for (int o = G / 2; o > 0; o >>= 1)
+    both = min2_nan<E>(both, __shfl_xor_sync(group, both, o));
+  const float2 ends = unpack2<E>(both);
+  const float lo = ends.x, hi = -ends.y;
   // The step rounded to 16 bits is the step that codes are made for and values read with;
   // the zero is one of the row's own values, so it needs no rounding. Each bound is divided
   // by itself: their difference may pass the largest bf16.
   constexpr float kFifteenth = 1.0f / 15.0f;
   const uint32_t sz = pack2<E>(__fsub_rn(__fmul_rn(hi, kFifteenth), __fmul_rn(lo, kFifteenth)), lo);
-  const float scale = scale_zero<E>(sz).x;
-  uint32_t code = 0;
-  if (scale > 0.0f) {
+  float x[16];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(x[k] - lo, scale)), 0.0f), 15.0f);
-      code |= static_cast<uint32_t>(c) << (4 * k);
-    }
+  for (int k = 0; k < 8; ++k) {
+    const float2 f = unpack2<E>(w[k]);
+    x[2 * k] = f.x;
+    x[2 * k + 1] = f.y;
   }
-  const long long row = page_row(id, which, hk, L.Hkv, L.shift) + (pos & (L.page - 1));
-  reinterpret_cast<uint32_t*>(L.codes + row * (D / 2))[lane] = code;
-  if (lane == 0) L.params[row] = sz;
+  const uint2 code = quantise<E>(x, lo, hi, scale_zero<E>(sz).x);
+  reinterpret_cast<uint2*>(p.L.codes + a.row * (D / 2))[a.lane] = code;
+  if (a.lane == 0) p.L.params[a.row] = sz;
 }
-
-// ------------------------------------------------------------------ read
 
 // The same rows back as 16-bit values [B, Hkv, n, D]; rows behind a count are zeros.
 template <int D, Elt E>
-__global__ void __launch_bounds__(256)
-    read_kernel(uint16_t* __restrict__ K, uint16_t* __restrict__ V, const Layout L,
-                const int* __restrict__ positions, const int* __restrict__ counts, int n,
-                long long rows) {
+__global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int G = D / 8;
-  const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;
-  const int lane = threadIdx.x % G, which = blockIdx.y;
-  if (r >= rows) return;
-  const int t = static_cast<int>(r % n);
-  const long long bh = r / n;
-  const int hk = static_cast<int>(bh % L.Hkv), b = static_cast<int>(bh / L.Hkv);
-  uint4 out = make_uint4(0u, 0u, 0u, 0u);
-  if (counts == nullptr || t < counts[b]) {
-    const long long pos = static_cast<long long>(positions[b]) + t;
-    const long long id = page_of(L.table + static_cast<size_t>(b) * L.max_pages, L.max_pages,
-                                 L.n_pages, L.shift, pos);
-    if (id < 0) {
-      if (lane == 0) atomicOr(&g_status, kStatusBadPage);
-    } else {
-      const long long row = page_row(id, which, hk, L.Hkv, L.shift) + (pos & (L.page - 1));
-      const uint32_t code = reinterpret_cast<const uint32_t*>(L.codes + row * (D / 2))[lane];
-      const float2 sz = scale_zero<E>(L.params[row]);
-      uint32_t o[4];
+  const RowAt<D> a = row_at<D>(p);
+  if (a.r >= p.rows) return;
+  uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  if (a.row >= 0) {
+    const uint2 code = reinterpret_cast<const uint2*>(p.L.codes + a.row * (D / 2))[a.lane];
+    const float2 sz = scale_zero<E>(p.L.params[a.row]);
+    // 2^23 + code, less 2^23
+    auto value = [&](uint32_t c, int k) {
+      return fmaf(sz.x, __uint_as_float(((c >> (4 * k)) & 15u) | 0x4B000000u) - 8388608.0f, sz.y);
+    };
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        o[k] = pack2<E>(fmaf(sz.x, static_cast<float>((code >> (8 * k)) & 15u), sz.y),
-                        fmaf(sz.x, static_cast<float>((code >> (8 * k + 4)) & 15u), sz.y));
-      out = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int k = 0; k < 4; ++k) {
+      o[k] = pack2<E>(value(code.x, 2 * k), value(code.x, 2 * k + 1));
+      o[4 + k] = pack2<E>(value(code.y, 2 * k), value(code.y, 2 * k + 1));
     }
   }
-  reinterpret_cast<uint4*>((which ? V : K) + r * D)[lane] = out;
+  uint4* dst = reinterpret_cast<uint4*>((a.which ? p.V : p.K) + static_cast<size_t>(a.r) * D) +
+               2 * a.lane;
+  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // ------------------------------------------------------------------ attend
@@ -183,11 +243,13 @@ __global__ void __launch_bounds__(256)
 // operands follow it. A code becomes a 16-bit float by a shift and one logical operation
 // (16 + code, the code placed in the mantissa of 16). With sum q = qs:
 //   s = scale_k * (sum q (16 + c)) + (zero_k - 16 scale_k) qs
-// and, with P' = P scale_v rounded to bf16 and codes brought to c - 8 (exact),
+// and, with P' = P scale_v and codes brought to c - 8 (exact),
 //   o = sum P' (c - 8) + sum (P zero_v + 8 P').
-// P' is bf16 for both element types: scales times weights of long rows would fall below
-// f16's normal range. The reference maximum of a row moves only when a score passes it by
-// more than 2^8, as in the forward.
+// P' enters its product as a sum of two bf16, P' rounded and what that leaves (2^-17 of P'
+// is lost): one bf16 alone put the output 2.4e-3 off in f16 (B1 H32 Hkv4 L131071 d128),
+// ten times that type's own rounding. f16 would not do: scales times weights of long rows
+// fall below its normal range. The reference maximum of a row moves only when a score
+// passes it by more than 2^8, as in the forward.
 // Bound by memory: d + 8 bytes per token and head (K and V).
 
 constexpr int kWarps = 4;
@@ -500,7 +562,7 @@ __global__ void __launch_bounds__(kWarps * 32)
           for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
       }
     }
-    uint32_t pb[NT][2];
+    uint32_t pb[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float w[4];
@@ -512,11 +574,13 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t pk = pack_bf16x2(w[2 * h] * vsz[h].x, w[2 * h + 1] * vsz[h].x);
+        const float a = w[2 * h] * vsz[h].x, b = w[2 * h + 1] * vsz[h].x;
+        const uint32_t pk = pack_bf16x2(a, b);
         const float2 back = unpack2<Elt::BF16>(pk);
-        z[nt][0] += fmaf(w[2 * h], vsz[h].y, 8.0f * back.x);
-        z[nt][1] += fmaf(w[2 * h + 1], vsz[h].y, 8.0f * back.y);
+        z[nt][0] += fmaf(w[2 * h], vsz[h].y, 8.0f * a);
+        z[nt][1] += fmaf(w[2 * h + 1], vsz[h].y, 8.0f * b);
         pb[nt][h] = transpose8(pk);
+        pb[nt][2 + h] = transpose8(pack_bf16x2(a - back.x, b - back.y));
       }
     }
 #pragma unroll
@@ -532,7 +596,10 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16n8k16_bf16(o[nt][4 * w + i], a[i], pb[nt][0], pb[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16n8k16_bf16(o[nt][4 * w + i], a[i], pb[nt][0], pb[nt][1]);
+          mma_16n8k16_bf16(o[nt][4 * w + i], a[i], pb[nt][2], pb[nt][3]);
+        }
     }
   }
 
@@ -592,41 +659,61 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// A row's pieces joined, by one warp a row: each lane D / 32 channels.
+// A row's pieces joined by a CTA of four warps: each thread four channels of every
+// (512 / D)-th piece, the sums joined over shared memory.
 template <int D, Elt E>
 __global__ void __launch_bounds__(128)
     combine_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                   uint16_t* __restrict__ O, float* __restrict__ LSE, long long rows,
-                   int n_pieces) {
+                   uint16_t* __restrict__ O, float* __restrict__ LSE, int n_pieces) {
+  constexpr int T = D / 4, S = 128 / T;  // threads of a piece, pieces at a time
+  __shared__ float sm_top[4], sm_sum[S];
+  __shared__ float4 sm_o[S][T];
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int C = D / 32;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
+  const size_t row = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = threadIdx.x % T, first = threadIdx.x / T;
   const float2* ml = part_ml + row * n_pieces;
   float top = -INFINITY;
-  for (int k = lane; k < n_pieces; k += 32) top = fmaxf(top, ml[k].x);
+  for (int k = threadIdx.x; k < n_pieces; k += 128) top = fmaxf(top, ml[k].x);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (lane == 0) sm_top[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(sm_top[0], sm_top[1]), fmaxf(sm_top[2], sm_top[3]));
   const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f, acc[C];
-#pragma unroll
-  for (int k = 0; k < C; ++k) acc[k] = 0.0f;
-  for (int k = 0; k < n_pieces; ++k) {
+  const float4* src = reinterpret_cast<const float4*>(part_o) + row * n_pieces * T + at;
+  float sum = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = first; k < n_pieces; k += S) {
     const float2 w = ml[k];
     if (w.y == 0.0f) continue;  // a piece without keys left its output unwritten
+    const float4 v = src[static_cast<size_t>(k) * T];
     const float f = ex2_approx(w.x - base);
     sum = fmaf(f, w.y, sum);
-    const float* v = part_o + (row * n_pieces + k) * D + lane * C;
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  }
+  sm_o[first][at] = acc;
+  if (at == 0) sm_sum[first] = sum;
+  __syncthreads();
+  if (first != 0) return;
 #pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+  for (int k = 1; k < S; ++k) {
+    const float4 v = sm_o[k][at];
+    sum += sm_sum[k];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint32_t* out = reinterpret_cast<uint32_t*>(O + row * D + lane * C);
-#pragma unroll
-  for (int i = 0; i < C / 2; ++i) out[i] = pack2<E>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  if (lane == 0) LSE[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+  reinterpret_cast<uint2*>(O + row * D)[at] =
+      make_uint2(pack2<E>(acc.x * inv, acc.y * inv), pack2<E>(acc.z * inv, acc.w * inv));
+  if (at == 0) LSE[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace cache4

@@ -1103,6 +1103,13 @@ fa_status make_layout(void* codes, void* params, const int32_t* table, int Hkv, 
   return FA_OK;
 }
 
+cache4::Divisor make_divisor(int n) {
+  int l = 0;
+  while ((1ll << l) < n) ++l;
+  const unsigned long long m = ((1ull << (31 + l)) + n - 1) / n;
+  return cache4::Divisor{static_cast<uint32_t>(n), static_cast<uint32_t>(m), 31 + l};
+}
+
 // Append (kAppend: K, V are read) and read back (K, V are written).
 template <Elt E, bool kAppend>
 fa_status cache4_rows_impl(const void* K, const void* V, void* codes, void* params,
@@ -1119,20 +1126,23 @@ fa_status cache4_rows_impl(const void* K, const void* V, void* codes, void* para
   if ((st = check_ptrs({K, V})) != FA_OK) return st;
   if (positions == nullptr || !aligned4(positions) || !aligned4(counts)) return FA_ERR_INVALID_ARG;
   if ((st = prepare_device()) != FA_OK) return st;
-  const dim3 grid(static_cast<unsigned>((rows * (d / 8) + 255) / 256), 2);
+  const dim3 grid(static_cast<unsigned>((rows * (d / 16) + 255) / 256), 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cache4::RowsParams p;
+  p.K = static_cast<uint16_t*>(const_cast<void*>(K));
+  p.V = static_cast<uint16_t*>(const_cast<void*>(V));
+  p.L = L;
+  p.positions = positions;
+  p.counts = counts;
+  p.n = make_divisor(n);
+  p.hkv = make_divisor(Hkv);
+  p.rows = static_cast<uint32_t>(rows);
   if constexpr (kAppend) {
-    const auto* k = static_cast<const uint16_t*>(K);
-    const auto* v = static_cast<const uint16_t*>(V);
-    if (d == 64)
-      return launch(cache4::append_kernel<64, E>, grid, 256, 0, s, k, v, L, positions, counts, n, rows);
-    return launch(cache4::append_kernel<128, E>, grid, 256, 0, s, k, v, L, positions, counts, n, rows);
+    if (d == 64) return launch(cache4::append_kernel<64, E>, grid, 256, 0, s, p);
+    return launch(cache4::append_kernel<128, E>, grid, 256, 0, s, p);
   } else {
-    auto* k = static_cast<uint16_t*>(const_cast<void*>(K));
-    auto* v = static_cast<uint16_t*>(const_cast<void*>(V));
-    if (d == 64)
-      return launch(cache4::read_kernel<64, E>, grid, 256, 0, s, k, v, L, positions, counts, n, rows);
-    return launch(cache4::read_kernel<128, E>, grid, 256, 0, s, k, v, L, positions, counts, n, rows);
+    if (d == 64) return launch(cache4::read_kernel<64, E>, grid, 256, 0, s, p);
+    return launch(cache4::read_kernel<128, E>, grid, 256, 0, s, p);
   }
 }
 
@@ -1142,7 +1152,7 @@ struct AttendPlan {
   int rows, nt, row_tiles, piece, n_pieces;
 };
 
-constexpr long long kAttendCtas = 148 * 8;  // CTAs that a call is cut into, if it is long enough
+constexpr long long kAttendCtas = 148 * 3;  // one wave (registers allow three CTAs per SM)
 constexpr int kMinPiece = 2 * cache4::kWarps;  // groups: two per warp
 
 AttendPlan attend_plan(int B, int H, int Hkv, int Nq, int max_len, int window_left) {
@@ -1154,7 +1164,8 @@ AttendPlan attend_plan(int B, int H, int Hkv, int Nq, int max_len, int window_le
   if (window_left >= 0) span = std::min<long long>(span, static_cast<long long>(window_left) + Nq + 15);
   const long long groups = (span + cache4::kGroup - 1) / cache4::kGroup;
   const long long heads = static_cast<long long>(B) * Hkv * a.row_tiles;
-  const long long want = std::max<long long>(1, (kAttendCtas + heads - 1) / heads);
+  const long long ctas = heads * 4 <= kAttendCtas ? kAttendCtas : 4 * kAttendCtas;
+  const long long want = (ctas + heads - 1) / heads;
   long long piece = std::max<long long>((groups + want - 1) / want, kMinPiece);
   piece = (piece + cache4::kWarps - 1) / cache4::kWarps * cache4::kWarps;
   a.piece = static_cast<int>(piece);
@@ -1171,9 +1182,9 @@ size_t attend_ws_bytes(const AttendPlan& a, int B, int H, int Nq, int d) {
 fa_status check_attend(int B, int H, int Hkv, int Nq, int d, int max_len) {
   if (B < 1 || H < 1 || Hkv < 1 || Nq < 0 || max_len < 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  // row indices and grids stay below 2^31, with up to kAttendCtas pieces a row
+  // row indices and grids stay below 2^31, with up to 4 kAttendCtas pieces a row
   if (static_cast<long long>(B) * H >= (1ll << 31) || Nq > (1 << 24) ||
-      static_cast<long long>(B) * H * std::max(Nq, 1) >= (1ll << 31) / kAttendCtas)
+      static_cast<long long>(B) * H * std::max(Nq, 1) >= (1ll << 31) / (4 * kAttendCtas))
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
@@ -1230,12 +1241,12 @@ fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* cod
     st = a.nt == 1 ? launch(cache4::attend_kernel<128, E, 1>, grid, T, 0, s, p)
                    : launch(cache4::attend_kernel<128, E, 2>, grid, T, 0, s, p);
   if (st != FA_OK || a.n_pieces == 1) return st;
-  const unsigned blocks = static_cast<unsigned>((rows + 3) / 4);
+  const unsigned blocks = static_cast<unsigned>(rows);
   if (d == 64)
     return launch(cache4::combine_kernel<64, E>, blocks, 128, 0, s, p.part_o, p.part_ml, p.O, LSE,
-                  rows, a.n_pieces);
+                  a.n_pieces);
   return launch(cache4::combine_kernel<128, E>, blocks, 128, 0, s, p.part_o, p.part_ml, p.O, LSE,
-                rows, a.n_pieces);
+                a.n_pieces);
 }
 
 }  // namespace
