@@ -562,9 +562,12 @@ def _masked(window, block_mask) -> bool:
     return window is not None or block_mask is not None
 
 
-def _scored(q, k, softcap, slopes, documents, prefix) -> bool:
+def _scored(q, k, window, block_mask, dropout, softcap, slopes, documents, prefix) -> bool:
+    """Whether a call takes the scored entry points; windows of f16 tensors do as well."""
     return (softcap is not None or slopes is not None or documents is not None
-            or prefix is not None or (k.dim() == 4 and k.shape[1] != q.shape[1]))
+            or prefix is not None or (k.dim() == 4 and k.shape[1] != q.shape[1])
+            or (q.dtype == torch.float16 and window is not None and block_mask is None
+                and dropout is None))
 
 
 def _check_scored(q, block_mask, dropout) -> str:
@@ -582,7 +585,7 @@ def forward(q, k, v, causal: bool = False, scale=None, window=None, block_mask=N
             dropout=None, softcap=None, slopes=None, documents=None, prefix=None):
     """(O, LSE) for bf16, f16 or fp32 q, k, v of shape [B, H, N, d] on the GPU.
     ``window`` / ``block_mask`` as for fa_forward_masked and ``dropout`` = (p, seed,
-    offset) as for fa_forward_dropout (bf16 only).
+    offset) as for fa_forward_dropout (bf16 only; ``window`` f16 too).
 
     Shaped scores (bf16 and f16, see fa_forward_scored in include/fa.h): ``softcap`` caps
     the scores by c * tanh(s / c); ``slopes`` (fp32 [H]) subtracts slopes[h] * |i - j|;
@@ -594,7 +597,7 @@ def forward(q, k, v, causal: bool = False, scale=None, window=None, block_mask=N
     scale = _default_scale(d, scale)
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    if _scored(q, k, softcap, slopes, documents, prefix):
+    if _scored(q, k, window, block_mask, dropout, softcap, slopes, documents, prefix):
         fn = fa_forward_scored_f16 if _check_scored(q, block_mask, dropout) else fa_forward_scored
         fn(q, k, v, o, lse, scale, causal, window, softcap, slopes, documents, prefix)
     elif dropout is not None:
@@ -630,7 +633,7 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale=None, workspace=No
     scale = _default_scale(d, scale)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ws = workspace_for(q) if workspace is None else workspace
-    if _scored(q, k, softcap, slopes, documents, prefix):
+    if _scored(q, k, window, block_mask, dropout, softcap, slopes, documents, prefix):
         fn = (fa_backward_scored_f16 if _check_scored(q, block_mask, dropout)
               else fa_backward_scored)
         fn(q, k, v, o, do, lse, dq, dk, dv, scale, causal, ws, window, softcap, slopes,

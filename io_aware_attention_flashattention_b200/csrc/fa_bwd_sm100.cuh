@@ -266,6 +266,117 @@ __global__ void __launch_bounds__(256)
   for (int k = lane; k < D / 4; k += 32) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+// The preprocess of shaped scores. D_i = rowsum(dO o O) takes O as rounded to 16 bits, and
+// that error, the same for all of a row's dS, shows where few keys share the weight: with
+// sharp scores over at most 16 keys dQ and dK came 0.5 to 0.65% off, twice what the rounding
+// of dS itself costs (a model of the roundings in 64 bits, q 4 N(0,1), cap 50). So for rows
+// of at most kFewKeys keys D is formed as sum_j P_ij dP_ij, from Q, K and V in 32 bits: 0.24%
+// for those, at most 0.41% for any window. The rows are N times the window at most.
+constexpr int kFewKeys = 16;
+
+struct PreParams {
+  const uint16_t* O;
+  const uint16_t* dO;
+  const uint16_t* Q;
+  const uint16_t* K;
+  const uint16_t* V;
+  const float* LSE;
+  float* L2;
+  float* Dv;
+  float* dQacc;
+  ScoreParams score;
+  float scale_log2;
+  int N, Npad, wl, wr;
+  long long total_rows;  // BH * Npad
+};
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// A lane's D / 32 channels of a row.
+template <int D, Elt E>
+__device__ __forceinline__ void lane_channels(float (&x)[D / 32], const uint16_t* row, int lane) {
+  const float2 a = unpack2<E>(reinterpret_cast<const uint32_t*>(row)[lane * (D / 64)]);
+  x[0] = a.x;
+  x[1] = a.y;
+  if constexpr (D == 128) {
+    const float2 b = unpack2<E>(reinterpret_cast<const uint32_t*>(row)[lane * 2 + 1]);
+    x[2] = b.x;
+    x[3] = b.y;
+  }
+}
+
+template <int D, Elt E>
+__global__ void __launch_bounds__(256) fa_bwd_pre_scored_kernel(const PreParams p) {
+  pdl_wait();  // the grid before this one (the forward) has completed
+  pdl_launch_dependents();
+  const long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= p.total_rows) return;
+  const int bh = static_cast<int>(r / p.Npad);
+  const int i = static_cast<int>(r - static_cast<long long>(bh) * p.Npad);
+  if (i >= p.N) {
+    if (lane == 0) {
+      p.L2[r] = INFINITY;
+      p.Dv[r] = 0.f;
+    }
+    return;
+  }
+  const size_t row = static_cast<size_t>(bh) * p.N + i;
+  float4* z = reinterpret_cast<float4*>(p.dQacc + row * D);
+#pragma unroll
+  for (int k = lane; k < D / 4; k += 32) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float lse = p.LSE[row];
+  const float l2 = (lse == -INFINITY) ? INFINITY : lse * 1.4426950408889634f;
+  const int b = bh / p.score.H;
+  const int* docs =
+      p.score.docs ? p.score.docs + static_cast<size_t>(b) * (p.score.n_docs + 1) : nullptr;
+  const int* prefix =
+      p.score.prefix ? p.score.prefix + static_cast<size_t>(b) * p.score.n_docs : nullptr;
+  const Span ks = keys_of_query(docs, prefix, p.score.n_docs, p.N, p.wl, p.wr, i);
+  float g[D / 32];
+  lane_channels<D, E>(g, p.dO + row * D, lane);
+  float d = 0.0f;
+  if (ks.hi - ks.lo <= kFewKeys && ks.hi > ks.lo) {
+    float q[D / 32], sum = 0.0f;
+    lane_channels<D, E>(q, p.Q + row * D, lane);
+    const size_t kv = static_cast<size_t>(bh / p.score.group) * p.N;
+    const float slope = p.score.slopes ? -p.score.slopes[bh % p.score.H] * p.score.slope_mul : 0.0f;
+    for (int j = ks.lo; j < ks.hi; ++j) {
+      float k[D / 32], v[D / 32], s = 0.0f, dp = 0.0f;
+      lane_channels<D, E>(k, p.K + (kv + j) * D, lane);
+      lane_channels<D, E>(v, p.V + (kv + j) * D, lane);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        s = fmaf(q[e], k[e], s);
+        dp = fmaf(g[e], v[e], dp);
+      }
+      s = warp_sum(s);
+      dp = warp_sum(dp);
+      // cap_in2 = 2 log2(e) scale / cap
+      if (p.score.cap_in2 != 0.0f) s = tanhf(s * (p.score.cap_in2 * 0.34657359027997264f));
+      const float u = fmaf(slope, fabsf(static_cast<float>(i - j)), s);
+      const float w = exp2f(fmaf(u, p.scale_log2, -l2));
+      sum += w;
+      d = fmaf(w, dp, d);
+    }
+    d /= sum;
+  } else {
+    float o[D / 32];
+    lane_channels<D, E>(o, p.O + row * D, lane);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) d = fmaf(o[e], g[e], d);
+    d = warp_sum(d);
+  }
+  if (lane == 0) {
+    p.Dv[r] = d;
+    p.L2[r] = l2;
+  }
+}
+
 // ------------------------------------------------------------------ dQ convert
 
 template <int D, Elt E>
@@ -292,14 +403,18 @@ __global__ void __launch_bounds__(256)
 // visible iff qoff + x < q_span (unsigned). ctr_head: the dropout counter's head word
 // (the call's head_base + the flattened head).
 // kScore: S^T is first brought to the shaped score (c turns it to log2 units); with a cap
-// dS takes the factor 1 - tanh^2, the derivative of the capped score by scale * q.k.
+// dS takes the factor 1 - tanh^2, the derivative of the capped score by scale * q.k. lone:
+// the query (counted from qh0) that sees this key alone, if any: its dS = P (dP - D) is 0
+// exactly, where dP and D, summed in different orders, would leave their rounding. Such a
+// query has the key's own index, and steps that hold one always test elements (kM).
 template <Elt E, bool kDropout, bool kM, int kScore = 0>
 __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const float4* Lv,
                                           const float4* Dv4, float c, int key, int qh0,
                                           uint32_t ctr_head,
                                           const DropoutParams& drop, int lane, int qoff,
                                           unsigned q_span, uint8_t* ds_row, int krow,
-                                          const ScoreParams& score, float slope_neg) {
+                                          const ScoreParams& score, float slope_neg,
+                                          int lone) {
   uint32_t sv[2][16], dv[2][16];
   tmem_ld16(tm_s, sv[0]);
   tmem_ld16(tm_dp, dv[0]);
@@ -369,6 +484,8 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
             const float y = __uint_as_float(th[k]);
             dsv[e] = fmaf(-y * y, dsv[e], dsv[e]);
           }
+          if constexpr (kScore != 0 && kM)
+            if (cc * 16 + k == lone) dsv[e] = 0.0f;
         }
       }
       pk[2 * v] = pack2<E>(pv[0], pv[1]);
@@ -670,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // queries that see this key row: [q_lo, q_hi) (empty for a padding key)
     int q_lo = (wr < 0) ? 0 : key - wr;
     int q_hi = (key >= p.N) ? q_lo : ((wl < 0) ? p.Npad + BM : key + wl + 1);
+    [[maybe_unused]] int lone = -1;  // kScore: the query that sees this key alone
     [[maybe_unused]] int full_lo = 0, full_hi = 0;  // kScore: queries that see all 32 keys
     if constexpr (kScore != 0) {
       const Span qs = queries_of_key(docs, prefix, p.score.n_docs, p.N, wl, wr, key);
@@ -678,6 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       q_hi = (qs.hi == p.N && qs.hi > qs.lo) ? p.Npad : qs.hi;
       full_lo = __reduce_max_sync(0xffffffffu, q_lo);
       full_hi = __reduce_min_sync(0xffffffffu, q_hi);
+      const Span ks = keys_of_query(docs, prefix, p.score.n_docs, p.N, wl, wr, key);
+      if (ks.hi - ks.lo == 1) lone = key;
     }
     const unsigned q_span = static_cast<unsigned>(q_hi - q_lo);
     const uint32_t ctr_head = p.drop.head_base + static_cast<uint32_t>(bh);  // dropout
@@ -717,11 +837,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // that cross a mask edge, none on all the others.
       if (mask)
         p_ds_half<E, kDropout, true, kScore>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop,
-                                             lane, qoff, q_span, ds_row, krow, p.score, slope_neg);
+                                             lane, qoff, q_span, ds_row, krow, p.score, slope_neg,
+                                             lone - qh0);
       else
         p_ds_half<E, kDropout, false, kScore>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop,
                                               lane, qoff, q_span, ds_row, krow, p.score,
-                                              slope_neg);
+                                              slope_neg, -1);
       tmem_wait_st();
       fence_proxy_async_smem();
       tc_fence_before();
@@ -1183,10 +1304,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qoff = qh0 - q_lo;
         if (mask)
           p_ds_half<E, kDropout, true>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
-                                       qoff, q_span, ds_row, krow, p.score, 0.0f);
+                                       qoff, q_span, ds_row, krow, p.score, 0.0f, -1);
         else
           p_ds_half<E, kDropout, false>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
-                                        qoff, q_span, ds_row, krow, p.score, 0.0f);
+                                        qoff, q_span, ds_row, krow, p.score, 0.0f, -1);
         tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();

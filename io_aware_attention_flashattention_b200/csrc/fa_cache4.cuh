@@ -238,22 +238,27 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
 // channels, as the 16 rows, so that up to 8 query rows cost one product:
 //   S^T[16 tokens x 8 rows] = codes[16 x d] Q^T[d x 8]
 //   O^T[d x 8] += V codes^T[d x 16] P^T[16 x 8]
-// Codes go from global memory to registers in the order the products take them: a thread
-// holds whole words of 8 codes and any order of the summed index will do, as long as both
-// operands follow it. A code becomes a 16-bit float by a shift and one logical operation
-// (16 + code, the code placed in the mantissa of 16). With sum q = qs:
-//   s = scale_k * (sum q (16 + c)) + (zero_k - 16 scale_k) qs
-// and, with P' = P scale_v and codes brought to c - 8 (exact),
+// A group's codes and pairs (2 * 8 d + 128 bytes) come through a ring of shared memory of
+// the warp's own, kStages - 1 groups ahead by asynchronous copies, and leave it in the order
+// that the products take them: a thread reads whole words of 8 codes, and any order of the
+// summed index will do as long as both operands follow it. Two codes of a word become a
+// pair of 16-bit floats 128 + code (bf16) or 1024 + code (f16) by a shift and one logical
+// operation, the code being the last bits of the mantissa, and c - 8 by one packed addition
+// (exact). With sum q = qs:
+//   s = scale_k * (sum q (c - 8)) + (zero_k + 8 scale_k) qs
+// and, with P' = P scale_v:
 //   o = sum P' (c - 8) + sum (P zero_v + 8 P').
 // P' enters its product as a sum of two bf16, P' rounded and what that leaves (2^-17 of P'
 // is lost): one bf16 alone put the output 2.4e-3 off in f16 (B1 H32 Hkv4 L131071 d128),
 // ten times that type's own rounding. f16 would not do: scales times weights of long rows
 // fall below its normal range. The reference maximum of a row moves only when a score
 // passes it by more than 2^8, as in the forward.
-// Bound by memory: d + 8 bytes per token and head (K and V).
+// Bound by memory (d + 8 bytes per token and head, K and V), then by the instructions that
+// unpack codes: shifts and logical operations issue at half rate.
 
 constexpr int kWarps = 4;
 constexpr int kGroup = 16;  // tokens per step of a warp
+constexpr int kStages = 4;
 
 struct AttendParams {
   const uint16_t* Q;  // [B, H, Nq, D]
@@ -273,21 +278,21 @@ struct AttendParams {
   float scale_log2;
 };
 
-__device__ __forceinline__ void mma_16n8k16_bf16(float (&c)[4], const uint32_t (&a)[4],
-                                                 uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_16n8k16_f16(float (&c)[4], const uint32_t (&a)[4],
-                                                uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <Elt E>
+__device__ __forceinline__ void mma_16n8k16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1) {
+  if constexpr (E == Elt::BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The 8 x 8 matrix of 16-bit elements that a warp holds as an accumulator's half, transposed.
@@ -297,76 +302,69 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-// Nibbles j of both halves of a word as a pair of 16-bit floats 16 + code.
+// Nibbles j of both halves of a word as a pair of 16-bit floats code - 8.
 template <Elt E, int j>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-  constexpr int s = (E == Elt::BF16 ? 3 : 6) - 4 * j;  // to the mantissa bits that count units
-  const uint32_t m = s >= 0 ? w << (s >= 0 ? s : 0) : w >> (s < 0 ? -s : 0);
-  constexpr uint32_t mask = E == Elt::BF16 ? 0x00780078u : 0x03C003C0u;
-  constexpr uint32_t sixteen = E == Elt::BF16 ? 0x41804180u : 0x4C004C00u;
-  return (m & mask) | sixteen;
-}
-
-// The same less 24: code - 8, exactly, in bf16.
-template <int j>
 __device__ __forceinline__ uint32_t centred(uint32_t w) {
   uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(nibbles<Elt::BF16, j>(w)), "r"(0xC1C0C1C0u));
+  if constexpr (E == Elt::BF16)
+    asm("add.rn.bf16x2 %0, %1, %2;"
+        : "=r"(r) : "r"(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u), "r"(0xC308C308u));
+  else
+    asm("add.rn.f16x2 %0, %1, %2;"
+        : "=r"(r) : "r"(((w >> (4 * j)) & 0x000F000Fu) | 0x64006400u), "r"(0xE408E408u));
   return r;
 }
 
-// What a warp holds of 16 tokens of one head: thread (g, t) = (lane / 4, lane % 4).
-template <int D>
-struct Piece {
-  uint32_t k[2][D / 32];  // rows g', g' + 8: channels t * D / 4 on
-  uint32_t v[4][D / 64];  // tokens t, 4 + t, 8 + t, 12 + t: channels g * D / 8 on
-  uint32_t kp[2], vp[2];  // (scale, zero) of tokens g', g' + 8
-};
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool wide) {
+  if (wide)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&r)[N], const uint8_t* p) {
-  if constexpr (N == 4) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-    r[0] = w.x; r[1] = w.y; r[2] = w.z; r[3] = w.w;
-  } else if constexpr (N == 2) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-    r[0] = w.x; r[1] = w.y;
-  } else {
-    r[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  }
+__device__ __forceinline__ void shared_words(uint32_t (&r)[N], uint32_t at) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(at));
 }
 
+// The ring's place of one 16-byte unit of a row, units of K and V moved within 128 bytes so
+// that the reads below meet no bank twice (K: rows g' of 8 lanes are 4 apart; V: the rows of
+// 16 lanes are 1 apart and half read).
 template <int D>
-__device__ __forceinline__ void load_piece(Piece<D>& x, const Layout& L, long long id, int hk,
-                                           int slot, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  const int own = (g >> 1) + (g & 1) * 4;  // the token of the product's row g
-  const long long kr = page_row(id, 0, hk, L.Hkv, L.shift) + slot;
-  const long long vr = page_row(id, 1, hk, L.Hkv, L.shift) + slot;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    load_words(x.k[h], L.codes + (kr + own + 8 * h) * (D / 2) + t * (D / 8));
-    x.kp[h] = __ldg(L.params + kr + own + 8 * h);
-    x.vp[h] = __ldg(L.params + vr + own + 8 * h);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    load_words(x.v[i], L.codes + (vr + 4 * i + t) * (D / 2) + g * (D / 16));
+__host__ __device__ constexpr int ring_unit(int which, int row, int unit) {
+  const int at = row * (D / 32) + unit;
+  return which == 0 ? at ^ (((row >> 2) & 1) << 2)
+                    : (D == 128 ? at ^ (((row >> 1) & 1) << 1) : at);
 }
 
-template <int D, Elt E, int NT>
+// kMods: kScoreCap and kScoreBias.
+template <int D, Elt E, int NT, int kMods>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_kernel(const AttendParams p) {
   constexpr int R = 8 * NT;      // query rows of the CTA
   constexpr int KS = D / 16;     // steps of the score product
   constexpr int MT = D / 16;     // 16-channel blocks of the output
-  __shared__ float sm_o[kWarps][R][D + 4];
-  __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
+  constexpr int kRow = D / 2;    // bytes of a row's codes
+  constexpr int kHalf = kGroup * kRow;      // of a group's K or V codes
+  constexpr int kStage = 2 * kHalf + 2 * kGroup * 4;
+  constexpr int kRing = kWarps * kStages * kStage;
+  constexpr int kJoin = kWarps * R * (D + 4 + 2) * 4;
+  // the ring, and after the loop the warps' results
+  __shared__ __align__(128) uint8_t smem[kRing > kJoin ? kRing : kJoin];
+  float (*const sm_o)[R][D + 4] = reinterpret_cast<float (*)[R][D + 4]>(smem);
+  float (*const sm_m)[R] = reinterpret_cast<float (*)[R]>(smem + kWarps * R * (D + 4) * 4);
+  float (*const sm_l)[R] = reinterpret_cast<float (*)[R]>(smem + kWarps * R * (D + 5) * 4);
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  long long at = blockIdx.x;
+  unsigned at = blockIdx.x;
   const int piece = static_cast<int>(at % p.n_pieces);
   at /= p.n_pieces;
   const int rt = static_cast<int>(at % p.row_tiles);
@@ -376,13 +374,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int n_rows = min(R, p.rows - row0);
   const int group = p.score.group;
   // the row of [B, H, Nq] that row r of this K/V head is
-  auto out_row = [&](int r) -> long long {
-    return (static_cast<long long>(b) * p.H + hk * group + r / p.Nq) * p.Nq + r % p.Nq;
+  auto out_row = [&](int r) -> size_t {
+    return (static_cast<size_t>(b) * p.H + hk * group + r / p.Nq) * p.Nq + r % p.Nq;
   };
 
-  const long long room = static_cast<long long>(p.L.max_pages) * p.L.page;
-  int len = p.lengths[b];
-  if (len < 0) len = 0;
+  const long long room = static_cast<long long>(p.L.max_pages) << p.L.shift;
+  int len = max(p.lengths[b], 0);
   if (len > room) {
     len = static_cast<int>(room);
     if (threadIdx.x == 0) atomicOr(&g_status, kStatusBadPage);
@@ -394,7 +391,6 @@ __global__ void __launch_bounds__(kWarps * 32)
 
   // this warp's groups: g_lo + piece * p.piece + warp, every kWarps-th of the piece, then the
   // same of piece + n_pieces, ... (more than one only where a length passes the given bound)
-  int grp = g_lo + piece * p.piece + warp, in_piece = 0;
   auto next = [&](int x, int& in) -> int {
     in += kWarps;
     x += kWarps;
@@ -404,6 +400,49 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     return x;
   };
+
+  // Copies of one group into a stage: a thread's units of the K and V codes (unit lane of
+  // each 512 bytes) and one of the 32 pairs. A group without a page takes page 0 instead (the
+  // reads stay inside the cache) and is marked.
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * kStage);
+  const unsigned page_groups = p.L.shift - 4;  // log2 of the groups per page
+  const unsigned n_pages = static_cast<unsigned>(p.L.n_pages);
+  const size_t v_rows = static_cast<size_t>(p.L.Hkv) << p.L.shift;  // from K's rows to V's
+  constexpr int kUnits = kHalf / 512;  // copies of a thread per half: 2 (D = 128) or 1
+  constexpr int kPerRow = D / 32;      // units of a row
+  unsigned bad = 0;                    // stages whose group has no page
+  auto issue = [&](int x, int stage) {
+    if (x < g_hi) {
+      unsigned id = static_cast<unsigned>(__ldg(table + (x >> page_groups)));
+      bad &= ~(1u << stage);
+      if (id >= n_pages) {
+        bad |= 1u << stage;
+        id = 0;
+      }
+      const size_t row = (static_cast<size_t>(id) * (2 * p.L.Hkv) + hk << p.L.shift) +
+                         ((x << 4) & (p.L.page - 1));
+      const uint8_t* k = p.L.codes + row * kRow + lane * 16;
+      const uint8_t* v = k + v_rows * kRow;
+      const uint32_t dst = ring + stage * kStage;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int unit = u * 32 + lane;
+        copy_async(dst + ring_unit<D>(0, unit / kPerRow, unit % kPerRow) * 16, k + u * 512, true);
+        copy_async(dst + kHalf + ring_unit<D>(1, unit / kPerRow, unit % kPerRow) * 16, v + u * 512,
+                   true);
+      }
+      copy_async(dst + 2 * kHalf + lane * 4,
+                 p.L.params + row + (lane & 15) + (lane < 16 ? 0 : v_rows), false);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int use = g_lo + piece * p.piece + warp, use_in = 0;
+  int ahead = use, ahead_in = 0;
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) {
+    issue(ahead, k);
+    ahead = next(ahead, ahead_in);
+  }
 
   // the queries, as the score product's second operand, and the sums of their channels
   uint32_t q[NT][KS][2];
@@ -439,11 +478,14 @@ __global__ void __launch_bounds__(kWarps * 32)
     for (int e = 0; e < 2; ++e) {
       const int r = min(row0 + nt * 8 + 2 * t + e, p.rows - 1);
       pos[nt][e] = pos0 + r % p.Nq;
-      slope_neg[nt][e] =
-          p.score.slopes ? -p.score.slopes[hk * group + r / p.Nq] * p.score.slope_mul : 0.0f;
+      if constexpr ((kMods & kScoreBias) != 0)
+        slope_neg[nt][e] =
+            -__ldg(p.score.slopes + hk * group + r / p.Nq) * p.score.slope_mul * p.scale_log2;
     }
 
+  // Without a cap the scores are in log2 units from the start: c goes into scale and zero.
   const float c = p.scale_log2;
+  const float c_in = (kMods & kScoreCap) ? 1.0f : c;
   float m[NT][2], l[NT][2], z[NT][2], o[NT][MT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -457,57 +499,58 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.0f;
   }
+  const int own = (g >> 1) + (g & 1) * 4;  // the token of the products' row g; g + 8: own + 8
+  const int edge_hi = pos0 - kGroup + 1, edge_lo = p.wl < 0 ? -1 : len - 1 - p.wl;
 
-  auto page_id = [&](int x) -> long long {
-    return x < g_hi ? page_of(table, p.L.max_pages, p.L.n_pages, p.L.shift,
-                              static_cast<long long>(x) * kGroup)
-                    : -1;
-  };
-  Piece<D> ahead;
-  long long id = page_id(grp);
-  load_piece(ahead, p.L, id < 0 ? 0 : id, hk, id < 0 ? 0 : (grp * kGroup) & (p.L.page - 1), lane);
-  while (grp < g_hi) {
-    const Piece<D> x = ahead;
-    const bool bad = id < 0;
-    const int k0 = grp * kGroup;
-    grp = next(grp, in_piece);
-    id = page_id(grp);
-    if (grp < g_hi)
-      load_piece(ahead, p.L, id < 0 ? 0 : id, hk, id < 0 ? 0 : (grp * kGroup) & (p.L.page - 1), lane);
-    if (bad) {  // tokens without a page are not there
+  for (int it = 0; use < g_hi; ++it) {
+    const int stage = it & (kStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // every lane's copies are in, and every lane is done with the stage before
+    issue(ahead, (it + kStages - 1) & (kStages - 1));
+    ahead = next(ahead, ahead_in);
+    const int k0 = use * kGroup;
+    use = next(use, use_in);
+    if ((bad >> stage) & 1u) {  // tokens without a page are not there
       if (lane == 0) atomicOr(&g_status, kStatusBadPage);
       continue;
     }
-    const int own = (g >> 1) + (g & 1) * 4;
-    float2 ksz[2], vsz[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      ksz[h] = scale_zero<E>(x.kp[h]);
-      vsz[h] = scale_zero<E>(x.vp[h]);
-      ksz[h].y = fmaf(-16.0f, ksz[h].x, ksz[h].y);
-    }
+    const uint32_t src = ring + stage * kStage;
     // scores: (token own + 8h, row 2t + e) is s[nt][2h + e]
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+    {
+      uint32_t k[2][D / 32];  // channels t * D / 4 on of the two tokens
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      const uint32_t a0[4] = {nibbles<E, 0>(x.k[0][w]), nibbles<E, 0>(x.k[1][w]),
-                              nibbles<E, 1>(x.k[0][w]), nibbles<E, 1>(x.k[1][w])};
-      const uint32_t a1[4] = {nibbles<E, 2>(x.k[0][w]), nibbles<E, 2>(x.k[1][w]),
-                              nibbles<E, 3>(x.k[0][w]), nibbles<E, 3>(x.k[1][w])};
+      for (int h = 0; h < 2; ++h) {
+        const int byte = t * (D / 8);
+        shared_words(k[h], src + ring_unit<D>(0, own + 8 * h, byte / 16) * 16 + byte % 16);
+      }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if constexpr (E == Elt::BF16) {
-          mma_16n8k16_bf16(s[nt], a0, q[nt][2 * w][0], q[nt][2 * w][1]);
-          mma_16n8k16_bf16(s[nt], a1, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
-        } else {
-          mma_16n8k16_f16(s[nt], a0, q[nt][2 * w][0], q[nt][2 * w][1]);
-          mma_16n8k16_f16(s[nt], a1, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+      for (int w = 0; w < D / 32; ++w) {
+        const uint32_t a0[4] = {centred<E, 0>(k[0][w]), centred<E, 0>(k[1][w]),
+                                centred<E, 1>(k[0][w]), centred<E, 1>(k[1][w])};
+        const uint32_t a1[4] = {centred<E, 2>(k[0][w]), centred<E, 2>(k[1][w]),
+                                centred<E, 3>(k[0][w]), centred<E, 3>(k[1][w])};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16n8k16<E>(s[nt], a0, q[nt][2 * w][0], q[nt][2 * w][1]);
+          mma_16n8k16<E>(s[nt], a1, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
         }
       }
+    }
+    float2 ksz[2], vsz[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[1];
+      shared_words(w, src + 2 * kHalf + (own + 8 * h) * 4);
+      ksz[h] = unpack2<E>(w[0]);
+      ksz[h].x *= c_in;
+      ksz[h].y = fmaf(ksz[h].y, c_in, 8.0f * ksz[h].x);
+      shared_words(w, src + 2 * kHalf + (kGroup + own + 8 * h) * 4);
+      vsz[h] = unpack2<E>(w[0]);
     }
     uint32_t u[4 * NT];
 #pragma unroll
@@ -516,38 +559,51 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int e = 0; e < 4; ++e)
         u[4 * nt + e] =
             __float_as_uint(fmaf(ksz[e >> 1].x, s[nt][e], ksz[e >> 1].y * qs[nt][e & 1]));
-    if (p.score.cap_in2 != 0.0f) tanh_scores(u, p.score);
+    if constexpr ((kMods & kScoreCap) != 0) {
+      tanh_scores(u, p.score);
+#pragma unroll
+      for (int e = 0; e < 4 * NT; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * c);
+    }
+    if constexpr ((kMods & kScoreBias) != 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          u[4 * nt + e] = __float_as_uint(
+              fmaf(slope_neg[nt][e & 1],
+                   static_cast<float>(pos[nt][e & 1] - (k0 + own + 8 * (e >> 1))),
+                   __uint_as_float(u[4 * nt + e])));
+    }
     // rows' keys are [pos - wl, pos]: tests only where the 16 tokens cross an edge
-    const bool edge = k0 + kGroup - 1 > pos0 || (p.wl >= 0 && k0 < len - 1 - p.wl);
+    if (k0 > edge_hi || k0 < edge_lo) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = k0 + own + 8 * h;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (key > pos[nt][e] || (p.wl >= 0 && key < pos[nt][e] - p.wl))
+              u[4 * nt + 2 * h + e] = __float_as_uint(-INFINITY);
+        // a token that no row sees has weight 0, whatever its slot holds
+        if (key >= len || (p.wl >= 0 && key < pos0 - p.wl)) vsz[h] = make_float2(0.0f, 0.0f);
+      }
+    }
     bool up = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int key = k0 + own + 8 * (e >> 1);
-        float y = __uint_as_float(u[4 * nt + e]);
-        if (p.score.slopes)
-          y = fmaf(slope_neg[nt][e & 1], static_cast<float>(pos[nt][e & 1] - key), y);
-        if (edge && (key > pos[nt][e & 1] || (p.wl >= 0 && key < pos[nt][e & 1] - p.wl)))
-          y = -INFINITY;
-        s[nt][e] = y;
-        up = up || y * c > m[nt][e & 1] + 8.0f;
+        s[nt][e] = __uint_as_float(u[4 * nt + e]);
+        up = up || s[nt][e] > m[nt][e & 1] + 8.0f;
       }
-    if (edge) {
-      // a token that no row sees has weight 0, whatever its slot holds
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = k0 + own + 8 * h;
-        if (key >= len || (p.wl >= 0 && key < pos0 - p.wl)) vsz[h] = make_float2(0.0f, 0.0f);
-      }
-    }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(s[nt][e], s[nt][2 + e]) * c;
+          float top = fmaxf(s[nt][e], s[nt][2 + e]);
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           const float now = fmaxf(m[nt][e], top);
@@ -569,7 +625,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float base = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
-        w[e] = ex2_approx(fmaf(s[nt][e], c, -base));
+        w[e] = ex2_approx(s[nt][e] - base);
         l[nt][e & 1] += w[e];
       }
 #pragma unroll
@@ -577,31 +633,41 @@ __global__ void __launch_bounds__(kWarps * 32)
         const float a = w[2 * h] * vsz[h].x, b = w[2 * h + 1] * vsz[h].x;
         const uint32_t pk = pack_bf16x2(a, b);
         const float2 back = unpack2<Elt::BF16>(pk);
-        z[nt][0] += fmaf(w[2 * h], vsz[h].y, 8.0f * a);
-        z[nt][1] += fmaf(w[2 * h + 1], vsz[h].y, 8.0f * b);
+        z[nt][0] = fmaf(8.0f, a, fmaf(w[2 * h], vsz[h].y, z[nt][0]));
+        z[nt][1] = fmaf(8.0f, b, fmaf(w[2 * h + 1], vsz[h].y, z[nt][1]));
         pb[nt][h] = transpose8(pk);
         pb[nt][2 + h] = transpose8(pack_bf16x2(a - back.x, b - back.y));
       }
     }
+    uint32_t v[4][D / 64];  // tokens t, 4 + t, 8 + t, 12 + t: channels g * D / 8 on
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int byte = g * (D / 16);
+      shared_words(v[i], src + kHalf + ring_unit<D>(1, 4 * i + t, byte / 16) * 16 + byte % 16);
+    }
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {
-      const uint32_t lo0 = __byte_perm(x.v[0][w], x.v[1][w], 0x5410);
-      const uint32_t lo1 = __byte_perm(x.v[2][w], x.v[3][w], 0x5410);
-      const uint32_t hi0 = __byte_perm(x.v[0][w], x.v[1][w], 0x7632);
-      const uint32_t hi1 = __byte_perm(x.v[2][w], x.v[3][w], 0x7632);
-      const uint32_t a[4][4] = {{centred<0>(lo0), centred<1>(lo0), centred<0>(lo1), centred<1>(lo1)},
-                                {centred<2>(lo0), centred<3>(lo0), centred<2>(lo1), centred<3>(lo1)},
-                                {centred<0>(hi0), centred<1>(hi0), centred<0>(hi1), centred<1>(hi1)},
-                                {centred<2>(hi0), centred<3>(hi0), centred<2>(hi1), centred<3>(hi1)}};
+      constexpr Elt B = Elt::BF16;
+      const uint32_t lo0 = __byte_perm(v[0][w], v[1][w], 0x5410);
+      const uint32_t lo1 = __byte_perm(v[2][w], v[3][w], 0x5410);
+      const uint32_t hi0 = __byte_perm(v[0][w], v[1][w], 0x7632);
+      const uint32_t hi1 = __byte_perm(v[2][w], v[3][w], 0x7632);
+      const uint32_t a[4][4] = {
+          {centred<B, 0>(lo0), centred<B, 1>(lo0), centred<B, 0>(lo1), centred<B, 1>(lo1)},
+          {centred<B, 2>(lo0), centred<B, 3>(lo0), centred<B, 2>(lo1), centred<B, 3>(lo1)},
+          {centred<B, 0>(hi0), centred<B, 1>(hi0), centred<B, 0>(hi1), centred<B, 1>(hi1)},
+          {centred<B, 2>(hi0), centred<B, 3>(hi0), centred<B, 2>(hi1), centred<B, 3>(hi1)}};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_16n8k16_bf16(o[nt][4 * w + i], a[i], pb[nt][0], pb[nt][1]);
-          mma_16n8k16_bf16(o[nt][4 * w + i], a[i], pb[nt][2], pb[nt][3]);
+          mma_16n8k16<B>(o[nt][4 * w + i], a[i], pb[nt][0], pb[nt][1]);
+          mma_16n8k16<B>(o[nt][4 * w + i], a[i], pb[nt][2], pb[nt][3]);
         }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();  // the ring is free
 
   // this warp's rows into shared memory: row 2t + e, channels g * D / 8 + 8w + 2i + (0, 1)
 #pragma unroll
@@ -644,9 +710,9 @@ __global__ void __launch_bounds__(kWarps * 32)
       acc.z = fmaf(f, v.z, acc.z);
       acc.w = fmaf(f, v.w, acc.w);
     }
-    const long long row = out_row(row0 + r);
+    const size_t row = out_row(row0 + r);
     if (p.n_pieces > 1) {
-      const long long slot = row * p.n_pieces + piece;
+      const size_t slot = row * p.n_pieces + piece;
       if (ch == 0) p.part_ml[slot] = make_float2(top, sum);
       if (sum > 0.0f || sum != sum) *reinterpret_cast<float4*>(p.part_o + slot * D + ch) = acc;
     } else {

@@ -1032,7 +1032,27 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
     return st;
   st = bwd_plan(ptrs, 9, B, H, N, d, scale, causal, workspace, workspace_bytes, &pl);
   if (st != FA_OK || N == 0) return st;
-  st = preprocess_impl<E>(O, dO, LSE, B, H, N, d, scale, causal, workspace, workspace_bytes, stream);
+  bwd::PreParams pre;
+  pre.O = static_cast<const uint16_t*>(O);
+  pre.dO = static_cast<const uint16_t*>(dO);
+  pre.Q = static_cast<const uint16_t*>(Q);
+  pre.K = static_cast<const uint16_t*>(K);
+  pre.V = static_cast<const uint16_t*>(V);
+  pre.LSE = LSE;
+  pre.L2 = pl.L2;
+  pre.Dv = pl.Dv;
+  pre.dQacc = pl.dQacc;
+  pre.score = p.score;
+  pre.scale_log2 = score_log2(scale, softcap);
+  pre.N = N;
+  pre.Npad = pl.Npad;
+  pre.wl = mask.wl;
+  pre.wr = mask.wr;
+  pre.total_rows = static_cast<long long>(pl.BH) * pl.Npad;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned pre_blocks = static_cast<unsigned>((pre.total_rows + 7) / 8);
+  st = d == 64 ? launch(bwd::fa_bwd_pre_scored_kernel<64, E>, pre_blocks, 256, 0, s, pre)
+               : launch(bwd::fa_bwd_pre_scored_kernel<128, E>, pre_blocks, 256, 0, s, pre);
   if (st != FA_OK) return st;
   CUtensorMap mq, mk, mv, mdo;
   const int BHkv = B * Hkv;
@@ -1065,7 +1085,6 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
                      ? 1
                      : 0;
   const unsigned grid = static_cast<unsigned>(n_tiles);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   constexpr int On = kScoreOn, Cap = kScoreCap, Bias = kScoreBias;
   switch (score_bits(softcap, slopes)) {
     case On: st = launch_bwd_scored<E, On>(d, grid, s, mq, mk, mv, mdo, p); break;
@@ -1189,6 +1208,16 @@ fa_status check_attend(int B, int H, int Hkv, int Nq, int d, int max_len) {
   return FA_OK;
 }
 
+template <Elt E, int kMods>
+fa_status launch_attend(int d, int nt, unsigned grid, cudaStream_t s, const cache4::AttendParams& p) {
+  constexpr int T = cache4::kWarps * 32;
+  if (d == 64)
+    return nt == 1 ? launch(cache4::attend_kernel<64, E, 1, kMods>, grid, T, 0, s, p)
+                   : launch(cache4::attend_kernel<64, E, 2, kMods>, grid, T, 0, s, p);
+  return nt == 1 ? launch(cache4::attend_kernel<128, E, 1, kMods>, grid, T, 0, s, p)
+                 : launch(cache4::attend_kernel<128, E, 2, kMods>, grid, T, 0, s, p);
+}
+
 template <Elt E>
 fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* codes,
                              const void* params, const int32_t* table, const int32_t* lengths,
@@ -1233,13 +1262,12 @@ fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* cod
   p.scale_log2 = score_log2(scale, softcap);
   const unsigned grid = static_cast<unsigned>(static_cast<long long>(B) * Hkv * a.row_tiles * a.n_pieces);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  constexpr int T = cache4::kWarps * 32;
-  if (d == 64)
-    st = a.nt == 1 ? launch(cache4::attend_kernel<64, E, 1>, grid, T, 0, s, p)
-                   : launch(cache4::attend_kernel<64, E, 2>, grid, T, 0, s, p);
-  else
-    st = a.nt == 1 ? launch(cache4::attend_kernel<128, E, 1>, grid, T, 0, s, p)
-                   : launch(cache4::attend_kernel<128, E, 2>, grid, T, 0, s, p);
+  switch (score_bits(softcap, slopes) & ~kScoreOn) {
+    case 0: st = launch_attend<E, 0>(d, a.nt, grid, s, p); break;
+    case kScoreCap: st = launch_attend<E, kScoreCap>(d, a.nt, grid, s, p); break;
+    case kScoreBias: st = launch_attend<E, kScoreBias>(d, a.nt, grid, s, p); break;
+    default: st = launch_attend<E, kScoreCap | kScoreBias>(d, a.nt, grid, s, p);
+  }
   if (st != FA_OK || a.n_pieces == 1) return st;
   const unsigned blocks = static_cast<unsigned>(rows);
   if (d == 64)
