@@ -290,90 +290,124 @@ struct PreParams {
   long long total_rows;  // BH * Npad
 };
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// A lane's D / 32 channels of a row.
-template <int D, Elt E>
-__device__ __forceinline__ void lane_channels(float (&x)[D / 32], const uint16_t* row, int lane) {
-  const float2 a = unpack2<E>(reinterpret_cast<const uint32_t*>(row)[lane * (D / 64)]);
-  x[0] = a.x;
-  x[1] = a.y;
-  if constexpr (D == 128) {
-    const float2 b = unpack2<E>(reinterpret_cast<const uint32_t*>(row)[lane * 2 + 1]);
-    x[2] = b.x;
-    x[3] = b.y;
-  }
-}
-
+// A warp takes 8 rows: D = rowsum(dO o O) with D / 8 lanes a row, 16 bytes each, and then, one
+// by one, the rows of few keys among them. Bound by memory (O, dO, and the zeroes of dQ's
+// accumulator: 8 D bytes a row).
 template <int D, Elt E>
 __global__ void __launch_bounds__(256) fa_bwd_pre_scored_kernel(const PreParams p) {
   pdl_wait();  // the grid before this one (the forward) has completed
   pdl_launch_dependents();
-  const long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  constexpr int kRows = 8, G = D / 8, S = 32 / G;  // lanes of a row, rows at a time
   const int lane = threadIdx.x & 31;
-  if (r >= p.total_rows) return;
-  const int bh = static_cast<int>(r / p.Npad);
-  const int i = static_cast<int>(r - static_cast<long long>(bh) * p.Npad);
-  if (i >= p.N) {
-    if (lane == 0) {
-      p.L2[r] = INFINITY;
-      p.Dv[r] = 0.f;
-    }
-    return;
-  }
-  const size_t row = static_cast<size_t>(bh) * p.N + i;
-  float4* z = reinterpret_cast<float4*>(p.dQacc + row * D);
+  const long long r = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kRows;
+  const int bh = static_cast<int>(r / p.Npad);  // Npad is a multiple of 128: one head's rows
+  const int i0 = static_cast<int>(r - static_cast<long long>(bh) * p.Npad);
+  const size_t row0 = static_cast<size_t>(bh) * p.N + i0;
+  const int n = min(kRows, p.N - i0);  // rows in front of N (may be negative)
+  uint4 o[kRows / S], g[kRows / S];
 #pragma unroll
-  for (int k = lane; k < D / 4; k += 32) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float lse = p.LSE[row];
-  const float l2 = (lse == -INFINITY) ? INFINITY : lse * 1.4426950408889634f;
+  for (int s = 0; s < kRows / S; ++s) {
+    const int k = s * S + lane / G;
+    o[s] = g[s] = make_uint4(0u, 0u, 0u, 0u);
+    if (k < n) {
+      o[s] = reinterpret_cast<const uint4*>(p.O + (row0 + k) * D)[lane % G];
+      g[s] = reinterpret_cast<const uint4*>(p.dO + (row0 + k) * D)[lane % G];
+    }
+  }
+  float4* z = reinterpret_cast<float4*>(p.dQacc + row0 * D);
+#pragma unroll
+  for (int s = 0; s < kRows * D / 128; ++s) {
+    const int k = s * 32 + lane;
+    if (k / (D / 4) < n) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // lane k < 8: row k's statistics and keys
+  float l2 = INFINITY, d = 0.0f;
+  Span ks{0, 0};
   const int b = bh / p.score.H;
   const int* docs =
       p.score.docs ? p.score.docs + static_cast<size_t>(b) * (p.score.n_docs + 1) : nullptr;
   const int* prefix =
       p.score.prefix ? p.score.prefix + static_cast<size_t>(b) * p.score.n_docs : nullptr;
-  const Span ks = keys_of_query(docs, prefix, p.score.n_docs, p.N, p.wl, p.wr, i);
-  float g[D / 32];
-  lane_channels<D, E>(g, p.dO + row * D, lane);
-  float d = 0.0f;
-  if (ks.hi - ks.lo <= kFewKeys && ks.hi > ks.lo) {
-    float q[D / 32], sum = 0.0f;
-    lane_channels<D, E>(q, p.Q + row * D, lane);
-    const size_t kv = static_cast<size_t>(bh / p.score.group) * p.N;
-    const float slope = p.score.slopes ? -p.score.slopes[bh % p.score.H] * p.score.slope_mul : 0.0f;
-    for (int j = ks.lo; j < ks.hi; ++j) {
-      float k[D / 32], v[D / 32], s = 0.0f, dp = 0.0f;
-      lane_channels<D, E>(k, p.K + (kv + j) * D, lane);
-      lane_channels<D, E>(v, p.V + (kv + j) * D, lane);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        s = fmaf(q[e], k[e], s);
-        dp = fmaf(g[e], v[e], dp);
-      }
-      s = warp_sum(s);
-      dp = warp_sum(dp);
-      // cap_in2 = 2 log2(e) scale / cap
-      if (p.score.cap_in2 != 0.0f) s = tanhf(s * (p.score.cap_in2 * 0.34657359027997264f));
-      const float u = fmaf(slope, fabsf(static_cast<float>(i - j)), s);
-      const float w = exp2f(fmaf(u, p.scale_log2, -l2));
-      sum += w;
-      d = fmaf(w, dp, d);
-    }
-    d /= sum;
-  } else {
-    float o[D / 32];
-    lane_channels<D, E>(o, p.O + row * D, lane);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) d = fmaf(o[e], g[e], d);
-    d = warp_sum(d);
+  if (lane < n) {
+    const float lse = p.LSE[row0 + lane];
+    if (lse != -INFINITY) l2 = lse * 1.4426950408889634f;
+    ks = keys_of_query(docs, prefix, p.score.n_docs, p.N, p.wl, p.wr, i0 + lane);
   }
-  if (lane == 0) {
-    p.Dv[r] = d;
-    p.L2[r] = l2;
+#pragma unroll
+  for (int s = 0; s < kRows / S; ++s) {
+    const uint32_t ow[4] = {o[s].x, o[s].y, o[s].z, o[s].w};
+    const uint32_t gw[4] = {g[s].x, g[s].y, g[s].z, g[s].w};
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = unpack2<E>(ow[k]), y = unpack2<E>(gw[k]);
+      sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+    }
+#pragma unroll
+    for (int w = G / 2; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    const float mine = __shfl_sync(0xffffffffu, sum, (lane % S) * G);
+    if (lane / S == s) d = mine;
+  }
+  // The rows of few keys, listed for the whole CTA: 64 rows that follow one another hold up
+  // to 64 of them at a document's start, which one warp would take one after the other.
+  __shared__ int n_few;
+  __shared__ int4 few[64];  // row, keys, log-sum-exp
+  __shared__ float few_d[64];
+  if (threadIdx.x == 0) n_few = 0;
+  __syncthreads();
+  int mine = -1;
+  if (ks.hi > ks.lo && ks.hi - ks.lo <= kFewKeys) {
+    mine = atomicAdd(&n_few, 1);
+    few[mine] = make_int4(i0 + lane, ks.lo, ks.hi, __float_as_int(l2));
+  }
+  __syncthreads();
+  const int heads_row = bh % p.score.H;
+  const float slope = p.score.slopes ? -p.score.slopes[heads_row] * p.score.slope_mul : 0.0f;
+  const size_t kv = static_cast<size_t>(bh / p.score.group) * p.N;
+  const size_t q_row = static_cast<size_t>(bh) * p.N;
+  for (int f = threadIdx.x >> 5; f < n_few; f += 8) {
+    // two lanes a key, half the channels each, 16 bytes at a time
+    const int4 w = few[f];
+    const int j = w.y + (lane >> 1);
+    const bool there = j < w.z;
+    const size_t half = (lane & 1) * (D / 2);
+    const uint4* q = reinterpret_cast<const uint4*>(p.Q + (q_row + w.x) * D + half);
+    const uint4* gr = reinterpret_cast<const uint4*>(p.dO + (q_row + w.x) * D + half);
+    const uint4* kk = reinterpret_cast<const uint4*>(p.K + (kv + (there ? j : w.y)) * D + half);
+    const uint4* v = reinterpret_cast<const uint4*>(p.V + (kv + (there ? j : w.y)) * D + half);
+    float s = 0.0f, dp = 0.0f;
+#pragma unroll 4
+    for (int e = 0; e < D / 16; ++e) {
+      const uint4 a = q[e], c = kk[e], x = gr[e], y = v[e];
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f1 = unpack2<E>(aw[k]), f2 = unpack2<E>(cw[k]);
+        const float2 f3 = unpack2<E>(xw[k]), f4 = unpack2<E>(yw[k]);
+        s = fmaf(f1.x, f2.x, fmaf(f1.y, f2.y, s));
+        dp = fmaf(f3.x, f4.x, fmaf(f3.y, f4.y, dp));
+      }
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    dp += __shfl_xor_sync(0xffffffffu, dp, 1);
+    // cap_in2 = 2 log2(e) scale / cap
+    if (p.score.cap_in2 != 0.0f) s = tanhf(s * (p.score.cap_in2 * 0.34657359027997264f));
+    s = fmaf(slope, fabsf(static_cast<float>(w.x - j)), s);
+    float weight = there ? exp2f(fmaf(s, p.scale_log2, -__int_as_float(w.w))) : 0.0f;
+    float acc = there ? weight * dp : 0.0f;
+#pragma unroll
+    for (int o2 = 2; o2 < 32; o2 <<= 1) {
+      weight += __shfl_xor_sync(0xffffffffu, weight, o2);
+      acc += __shfl_xor_sync(0xffffffffu, acc, o2);
+    }
+    if (lane == 0) few_d[f] = acc / weight;
+  }
+  __syncthreads();
+  if (mine >= 0) d = few_d[mine];
+  if (lane < kRows) {
+    p.L2[r + lane] = l2;
+    p.Dv[r + lane] = d;
   }
 }
 
@@ -415,6 +449,13 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
                                           unsigned q_span, uint8_t* ds_row, int krow,
                                           const ScoreParams& score, float slope_neg,
                                           int lone) {
+  // kScore: the queries [-qoff, -qoff + q_span) of the half that see this key, as bits
+  [[maybe_unused]] uint32_t seen[2] = {0u, 0u};
+  if constexpr (kScore != 0 && kM) {
+    const int hi = static_cast<int>(q_span) - qoff;
+    seen[0] = span_bits(-qoff, hi);
+    seen[1] = span_bits(-qoff - 32, hi - 32);
+  }
   uint32_t sv[2][16], dv[2][16];
   tmem_ld16(tm_s, sv[0]);
   tmem_ld16(tm_dp, dv[0]);
@@ -429,7 +470,7 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
     // tanh of the chunk's scores, kept apart from the bias for the derivative
     [[maybe_unused]] uint32_t th[(kScore & kScoreCap) ? 16 : 1];
     if constexpr ((kScore & kScoreCap) != 0) {
-      tanh_scores(sv[cur], score);
+      tanh_scores<16>(sv[cur], score);
 #pragma unroll
       for (int k = 0; k < 16; ++k) th[k] = sv[cur][k];
     }
@@ -458,6 +499,37 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
       transpose4_lanes(zq, u);
     }
     uint32_t pk[8], dk[8];
+    if constexpr (kScore != 0) {
+      // in pairs: P = 2^(S c - L2), dS = P (dP - D) (1 - tanh^2)
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        const int k = 2 * v;
+        const float4 L4 = Lv[cc * 4 + v / 2], D4 = Dv4[cc * 4 + v / 2];
+        const float2 nl = (v & 1) ? make_float2(-L4.z, -L4.w) : make_float2(-L4.x, -L4.y);
+        const float2 nd = (v & 1) ? make_float2(-D4.z, -D4.w) : make_float2(-D4.x, -D4.y);
+        const float2 x = ffma2(make_float2(__uint_as_float(sv[cur][k]),
+                                           __uint_as_float(sv[cur][k + 1])),
+                               make_float2(c, c), nl);
+        float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        if constexpr (kM) {
+          const uint32_t bits = seen[cc / 2] >> ((cc & 1) * 16 + k);
+          if ((bits & 1u) == 0u) pe.x = 0.f;
+          if ((bits & 2u) == 0u) pe.y = 0.f;
+        }
+        float2 ds = fmul2(pe, fadd2(make_float2(__uint_as_float(dv[cur][k]),
+                                                __uint_as_float(dv[cur][k + 1])), nd));
+        if constexpr ((kScore & kScoreCap) != 0) {
+          const float2 y = make_float2(__uint_as_float(th[k]), __uint_as_float(th[k + 1]));
+          ds = fmul2(ds, ffma2(make_float2(-y.x, -y.y), y, make_float2(1.0f, 1.0f)));
+        }
+        if constexpr (kM) {
+          if (cc * 16 + k == lone) ds.x = 0.0f;
+          if (cc * 16 + k + 1 == lone) ds.y = 0.0f;
+        }
+        pk[v] = pack2<E>(pe.x, pe.y);
+        dk[v] = pack2<E>(ds.x, ds.y);
+      }
+    } else {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const float4 L4 = Lv[cc * 4 + v];
@@ -480,18 +552,13 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
         } else {
           pv[e] = pe;
           dsv[e] = pe * (__uint_as_float(dv[cur][k]) - Ds[e]);
-          if constexpr ((kScore & kScoreCap) != 0) {
-            const float y = __uint_as_float(th[k]);
-            dsv[e] = fmaf(-y * y, dsv[e], dsv[e]);
-          }
-          if constexpr (kScore != 0 && kM)
-            if (cc * 16 + k == lone) dsv[e] = 0.0f;
         }
       }
       pk[2 * v] = pack2<E>(pv[0], pv[1]);
       pk[2 * v + 1] = pack2<E>(pv[2], pv[3]);
       dk[2 * v] = pack2<E>(dsv[0], dsv[1]);
       dk[2 * v + 1] = pack2<E>(dsv[2], dsv[3]);
+    }
     }
     tmem_st8(tm_s + 8 * cc, pk);
     tmem_st8(tm_dp + 8 * cc, dk);

@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         u[4 * nt + e] =
             __float_as_uint(fmaf(ksz[e >> 1].x, s[nt][e], ksz[e >> 1].y * qs[nt][e & 1]));
     if constexpr ((kMods & kScoreCap) != 0) {
-      tanh_scores(u, p.score);
+      tanh_scores<4 * NT>(u, p.score);
 #pragma unroll
       for (int e = 0; e < 4 * NT; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * c);
     }

@@ -48,6 +48,7 @@ namespace fwd {
 constexpr int BM = 128;        // query rows per tile
 constexpr int BN = 128;        // key/value rows per tile
 constexpr int kThreads = 352;  // 8 softmax warps, K/Q producer, MMA, V producer
+constexpr int kThreadsScore = 608;  // kScore instances: 16 softmax warps and the same others
 constexpr int kWarpTmaK = 8;
 constexpr int kWarpMma = 9;
 constexpr int kWarpTmaV = 10;
@@ -183,10 +184,8 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
 // - m_ref), their sum l and, rounded to 16 bits, P_t into the swizzled shared tile (with
 // dropout applied after the sum); then PFull. n counts this tile's S and PV products
 // before this one (their barrier phases); first: no PV_t of the item yet. Returns false
-// if a bounded wait gave up. kScore: S is first brought to the shaped score, in units that
-// scale_log2 turns to log2 (see ScoreParams), chunk by chunk as it leaves TMEM; the row's
-// visible keys come from rs instead of wl and wr.
-template <int D, Elt E, bool kDropout, int kScore = 0>
+// if a bounded wait gave up.
+template <int D, Elt E, bool kDropout>
 __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog& wd,
                                                  uint32_t tm_s, uint32_t tm_o, uint8_t* p_row,
                                                  uint32_t bar_sfree, uint32_t bar_pvdone,
@@ -194,13 +193,13 @@ __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog
                                                  int r0, int row, int row_in_tile, int wl,
                                                  int wr, uint32_t ctr_head, int lane,
                                                  int wq, int t, float& m_ref, float& l,
-                                                 float& lr, const RowScore& rs) {
+                                                 float& lr) {
   using C = Cfg<D>;
   const float c = p.scale_log2;
   const int r1 = r0 + BM - 1;
   // visible keys of this row: [k_lo, k_hi)
-  const int k_lo = kScore ? rs.k_lo : ((wl < 0) ? 0 : row - wl);
-  const int k_hi = kScore ? rs.k_hi : ((wr < 0) ? p.N : min(p.N, row + wr + 1));
+  const int k_lo = (wl < 0) ? 0 : row - wl;
+  const int k_hi = (wr < 0) ? p.N : min(p.N, row + wr + 1);
   tc_fence_after();
   uint32_t s[4][32];
 #pragma unroll
@@ -212,18 +211,9 @@ __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog
   if (lane == 0) mbar_arrive(bar_sfree);
   if (wq == 0) FA_TRACE_POINT(52, n, t);
   const int kv0 = kt * BN;
-  if constexpr ((kScore & kScoreCap) != 0) {
-#pragma unroll
-    for (int cc = 0; cc < 4; ++cc) tanh_scores(s[cc], p.score);
-  }
-  if constexpr ((kScore & kScoreBias) != 0) {
-#pragma unroll
-    for (int cc = 0; cc < 4; ++cc) bias_scores(s[cc], kv0 + 32 * cc - row, rs.slope_neg);
-  }
   // masking only where the tile crosses an edge of some row's visible range
-  const bool need_mask = kScore ? (kv0 < rs.full_lo || kv0 + BN > rs.full_hi)
-                                : ((kv0 + BN > p.N) || (wr >= 0 && kv0 + BN - 1 > r0 + wr) ||
-                                   (wl >= 0 && kv0 < r1 - wl));
+  const bool need_mask = (kv0 + BN > p.N) || (wr >= 0 && kv0 + BN - 1 > r0 + wr) ||
+                         (wl >= 0 && kv0 < r1 - wl);
   if (need_mask) {
     // key kv0 + k is visible iff 0 <= kv0 + k - k_lo < k_hi - k_lo
     const int off = kv0 - k_lo;
@@ -349,8 +339,219 @@ __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog
   return true;
 }
 
+// Shaped scores: the softmax of a query tile by eight warps, two threads a row, 64 columns of
+// each key tile each. Shaping adds up to two thirds to the softmax's instructions, and with
+// one thread a row (two such warps per scheduler) their latency bounds it, or the fetching of
+// its unrolled forms. B1 H8 N16384 d128 causal forward, q 4 N(0, 1): cap 50 / 20 / 5 in the
+// best of five arrangements of one thread a row 0.79 / 1.06 / 1.39 ms (0.72 / 1.75 / 1.95 in
+// one that favoured scores far inside the cap), this way 0.75 / 0.84 / 1.11 ms; bias 0.69 ->
+// 0.64 ms, documents alone 0.49 ms either way (plain causal 0.47 ms). The two threads of a row
+// trade their maxima through TMEM: each writes its own to the first of its 64 columns of
+// S_t, which it has read by then. What bounds it now: issue (2.1 instructions per cycle with
+// a cap; the tensor pipe is 36% active).
+//
+// One key tile: what softmax_key_tile does, for columns [64 half, 64 half + 64).
+//   cap: tanh ascends, so the maximum may be taken of the raw scores, and the polynomial of
+//     tanh, with c in it, goes straight into the exponent's FFMA (fused) where the tile needs
+//     no element tests and all scores of the warp lie within its reach; else tanh in place.
+//   bias: where the tile lies on one side of the warp's rows, slope_neg |distance| is base +
+//     sl (16 g + e) for column e of group g of 16: the scores get sl e, and base + 16 sl g
+//     comes with the group's maximum and exponents.
+template <int D, Elt E, int kScore>
+__device__ __forceinline__ bool scored_half_tile(const Params& p, const Watchdog& wd,
+                                                 uint32_t tm_s, uint32_t tm_o, uint8_t* p_row,
+                                                 uint32_t bar_sfree, uint32_t bar_trade,
+                                                 uint32_t bar_pvdone, uint32_t bar_pfull, int n,
+                                                 int half, int kt, int row_lo, int row,
+                                                 int row_in_tile, int lane, float& m_ref,
+                                                 float& l, float& lr, const RowScore& rs) {
+  using C = Cfg<D>;
+  constexpr bool kCap = (kScore & kScoreCap) != 0, kBias = (kScore & kScoreBias) != 0;
+  const float c = p.scale_log2;
+  const int col0 = 64 * half, k0 = kt * BN + col0;  // this thread's first column and key
+  const bool need_mask = k0 < rs.full_lo || k0 + 64 > rs.full_hi;
+  auto pair = [](const uint32_t* x) {
+    return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  };
+  auto put = [](uint32_t* x, float2 v) {
+    x[0] = __float_as_uint(v.x);
+    x[1] = __float_as_uint(v.y);
+  };
+  tc_fence_after();
+  uint32_t s[2][32];
+  tmem_ld32(tm_s + col0, s[0]);
+  tmem_ld32(tm_s + col0 + 32, s[1]);
+  tmem_wait_ld();
+  [[maybe_unused]] bool fused = false;
+  float top = -INFINITY;
+  if constexpr (kCap && !kBias) {
+    float a[4], b[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t* x = &s[q / 2][(q & 1) * 16];
+      a[q] = b[q] = __uint_as_float(x[15]);
+#pragma unroll
+      for (int k = 0; k < 14; k += 2) {
+        a[q] = fmax3(a[q], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+        b[q] = fmin3(b[q], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+      }
+      a[q] = fmaxf(a[q], __uint_as_float(x[14]));
+      b[q] = fminf(b[q], __uint_as_float(x[14]));
+    }
+    top = fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
+    const float most = fmaxf(top, -fminf(fmin3(b[0], b[1], b[2]), b[3]));
+    fused = !need_mask && __all_sync(0xffffffffu, most * most <= p.score.lim5);
+  }
+  if constexpr (kCap) {
+    if (!fused) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tanh_scores<16>(&s[q / 2][(q & 1) * 16], p.score);
+    }
+  }
+  float base = 0.0f, sl = 0.0f;
+  if constexpr (kBias) {
+    const bool right = k0 >= row_lo + 31;
+    if (right || k0 + 63 <= row_lo) {
+      sl = right ? rs.slope_neg : -rs.slope_neg;
+      base = static_cast<float>(k0 - row) * sl;
+      float2 e8[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        e8[e] = make_float2(sl * static_cast<float>(2 * e), sl * static_cast<float>(2 * e + 1));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) put(&s[i][2 * k], fadd2(pair(&s[i][2 * k]), e8[k & 7]));
+    } else {
+      const float f0 = static_cast<float>(k0 - row);
+#pragma unroll
+      for (int k = 0; k < 64; ++k)
+        s[k / 32][k % 32] =
+            __float_as_uint(fmaf(rs.slope_neg, fabsf(f0 + static_cast<float>(k)),
+                                 __uint_as_float(s[k / 32][k % 32])));
+    }
+  }
+  if (need_mask) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t seen = span_bits(rs.k_lo - k0 - 32 * i, rs.k_hi - k0 - 32 * i);
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (((seen >> k) & 1u) == 0u) s[i][k] = __float_as_uint(-INFINITY);
+    }
+  }
+  float mx2;  // the maximum in log2 units
+  if (kCap && !kBias && fused) {
+    mx2 = odd_poly(top, p.score.cq5);
+  } else {
+    float gm[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t* x = &s[g / 2][(g & 1) * 16];
+      float t1[5];
+#pragma unroll
+      for (int q = 0; q < 5; ++q)
+        t1[q] = fmax3(__uint_as_float(x[3 * q]), __uint_as_float(x[3 * q + 1]),
+                      __uint_as_float(x[3 * q + 2]));
+      gm[g] = fmax3(fmax3(t1[0], t1[1], t1[2]), fmaxf(t1[3], t1[4]), __uint_as_float(x[15]));
+      if constexpr (kBias) gm[g] = fmaf(16.0f * g, sl, gm[g]);
+    }
+    mx2 = (fmaxf(fmax3(gm[0], gm[1], gm[2]), gm[3]) + base) * c;
+  }
+  // trade maxima with the row's other thread; then S_t may be overwritten
+  tmem_st1(tm_s + col0, __float_as_uint(mx2));
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar_trade);
+  if (!__all_sync(0xffffffffu, mbar_wait(bar_trade, n & 1, wd))) return false;
+  tc_fence_after();
+  mx2 = fmaxf(mx2, __uint_as_float(tmem_ld1(tm_s + (64 - col0))));
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar_sfree);
+  const float m_new = fmaxf(m_ref, mx2);
+  const bool need = m_new > m_ref + kRescaleThreshold;
+  // as in softmax_key_tile: the reference max moves for the whole warp when any row needs it
+  // (the same for both warps of the rows)
+  const bool move = __any_sync(0xffffffffu, need);
+  float alpha = 1.0f;
+  if (move) {
+    alpha = (m_ref == -INFINITY) ? 0.0f : ex2_approx(m_ref - m_new);
+    m_ref = m_new;
+    l *= alpha;
+    lr *= alpha;
+  }
+  const float m_use = (m_ref == -INFINITY) ? 0.0f : m_ref;
+  // the exponents
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float nm = -m_use;
+      if constexpr (kBias) nm = fmaf(fmaf(32.0f * i + 16.0f * g, sl, base), c, nm);
+      const float2 nm2 = make_float2(nm, nm);
+      if (kCap && !kBias && fused) {
+#pragma unroll
+        for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+          const float2 v = pair(&s[i][k]);
+          put(&s[i][k], ffma2(v, odd_poly2(fmul2(v, v), p.score.cq5), nm2));
+        }
+      } else {
+#pragma unroll
+        for (int k = 16 * g; k < 16 * g + 16; k += 2)
+          put(&s[i][k], ffma2(pair(&s[i][k]), make_float2(c, c), nm2));
+      }
+    }
+  // the previous PV_t must be complete before P_t is overwritten and O_t rescaled
+  if (n > 0) {
+    if (!__all_sync(0xffffffffu, mbar_wait(bar_pvdone, (n - 1) & 1, wd))) return false;
+    tc_fence_after();
+  }
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 accr[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint8_t* chunk = p_row + half * C::kChunkBytes;  // this thread's 128 bytes of P
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t pk[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = pair(&s[i][8 * u + 2 * k]);
+        const float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        acc[k & 1] = fadd2(acc[k & 1], pe);
+        pk[k] = pack2<E>(pe.x, pe.y);
+        accr[k & 1] = fadd2(accr[k & 1], unpack2<E>(pk[k]));
+      }
+      *reinterpret_cast<uint4*>(chunk + (((i * 4 + u) ^ (row_in_tile & 7)) * 16)) =
+          make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    }
+  l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+  lr += (accr[0].x + accr[0].y) + (accr[1].x + accr[1].y);
+  if (move && n > 0) {
+    // bring the sum up to the previous key tile to the new reference max before this PV_t:
+    // half of O_t's columns
+#pragma unroll 1
+    for (int cc = half * (D / 64); cc < (half + 1) * (D / 64); ++cc) {
+      uint32_t o[32];
+      tmem_ld32(tm_o + cc * 32, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+      tmem_st32(tm_o + cc * 32, o);
+    }
+    tmem_wait_st();
+  }
+  fence_proxy_async_smem();  // P (generic stores) before the MMA reads it
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar_pfull);
+  return true;
+}
+
 template <int D, Elt E, bool kMasked, bool kDropout = false, int kScore = 0>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kScore ? kThreadsScore : kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const Params p) {
   using C = Cfg<D>;
@@ -364,6 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
 
+  constexpr int kSoftWarps = kScore ? 16 : 8;
+  constexpr int kWarpTmaK = kSoftWarps, kWarpMma = kSoftWarps + 1, kWarpTmaV = kSoftWarps + 2;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // Without a window's left bound or a block mask (kMasked = false) those are
@@ -444,8 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(C::kBarQFull + t), 1);
       mbar_init(bar(C::kBarSFull + t), 1);
-      mbar_init(bar(C::kBarSFree + t), 4);  // one arrival per softmax warp
-      mbar_init(bar(C::kBarPFull + t), 4);
+      mbar_init(bar(C::kBarSFree + t), kSoftWarps / 2);  // one arrival per softmax warp
+      mbar_init(bar(C::kBarPFull + t), kSoftWarps / 2);
+      if constexpr (kScore != 0) mbar_init(bar(C::kBarOFree + t), 8);  // maxima traded
       mbar_init(bar(C::kBarPVDone + t), 1);
     }
     for (int s = 0; s < C::kKSlots; ++s) {
@@ -614,6 +818,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     drain_wait(bar(C::kBarDrain), 0, p.timeout_ns);
     __syncwarp();
     FA_TRACE_POINT(99, 0, 0);
+  } else if constexpr (kScore != 0) {
+    // ------------------------------------------------------------ softmax, two threads a row
+    const int t = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3;
+    const int row_in_tile = wq * 32 + lane;
+    const int r0 = q0 + t * BM, row = r0 + row_in_tile;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tm_s = tmem + lane_off + C::kTmS0 + t * 128;
+    const uint32_t tm_o = tmem + lane_off + C::kTmO0 + t * D;
+    uint8_t* p_row = base_ptr + C::kPOff + t * C::kPBytes + row_in_tile * 128;
+    const uint32_t bar_trade = bar(C::kBarOFree + t);
+    const int t_lo = t ? lo[1] : lo[0], t_nk = t ? nk[1] : nk[0];
+    RowScore rs{};
+    const Span ks = keys_of_query(docs, prefix, p.score.n_docs, p.N, wl, wr, row);
+    rs.k_lo = ks.lo;
+    rs.k_hi = ks.hi;
+    // rows behind N are not written: they ask for no element tests
+    rs.full_lo = __reduce_max_sync(0xffffffffu, row < p.N ? ks.lo : 0);
+    rs.full_hi = __reduce_min_sync(0xffffffffu, row < p.N ? ks.hi : p.N);
+    if constexpr ((kScore & kScoreBias) != 0)
+      rs.slope_neg = -p.score.slopes[bh % p.score.H] * p.score.slope_mul;
+    float m_ref = -INFINITY;
+    float l = 0.0f, lr = 0.0f;  // this thread's columns' part (lr: of P as rounded, see below)
+    bool ok = t_nk > 0;
+    for (int j = 0; j < t_nk && ok; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kBarSFull + t), j & 1, wd));
+      if (!ok) break;
+      ok = scored_half_tile<D, E, kScore>(p, wd, tm_s, tm_o, p_row, bar(C::kBarSFree + t),
+                                          bar_trade, bar(C::kBarPVDone + t),
+                                          bar(C::kBarPFull + t), j, half, t_lo + j, r0 + wq * 32,
+                                          row, row_in_tile, lane, m_ref, l, lr, rs);
+    }
+    // both threads of a row take its whole sums, traded like the maxima
+    if (ok) {
+      // (in columns of their own: the other thread may not have read the last maximum yet)
+      tmem_st1(tm_s + 64 * half + 1, __float_as_uint(l));
+      tmem_st1(tm_s + 64 * half + 2, __float_as_uint(lr));
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_trade);
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_trade, t_nk & 1, wd));
+    }
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kBarPVDone + t), (t_nk - 1) & 1, wd));
+    const bool mine = row < p.N && (t == 0 || own1);
+    uint16_t* orow = p.O + (static_cast<size_t>(bh) * p.N + row) * D + half * (D / 2);
+    if (t_nk == 0 && mine) {
+      // a query tile that sees no key: O = 0, LSE = -inf
+#pragma unroll
+      for (int v = 0; v < D / 16; ++v)
+        reinterpret_cast<uint4*>(orow)[v] = make_uint4(0u, 0u, 0u, 0u);
+      if (half == 0) p.LSE[static_cast<size_t>(bh) * p.N + row] = -INFINITY;
+    }
+    if (ok) {
+      tc_fence_after();
+      l += __uint_as_float(tmem_ld1(tm_s + 65 - 64 * half));
+      lr += __uint_as_float(tmem_ld1(tm_s + 66 - 64 * half));
+      const float inv_l = (lr > 0.0f) ? 1.0f / lr : 0.0f;
+#pragma unroll
+      for (int cc = 0; cc < D / 64; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(tm_o + half * (D / 2) + cc * 32, o);
+        tmem_wait_ld();
+        if (mine) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pk[k] = pack2<E>(__uint_as_float(o[8 * v + 2 * k]) * inv_l,
+                               __uint_as_float(o[8 * v + 2 * k + 1]) * inv_l);
+            reinterpret_cast<uint4*>(orow + cc * 32)[v] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        }
+      }
+      if (mine && half == 0)
+        p.LSE[static_cast<size_t>(bh) * p.N + row] =
+            (l > 0.0f) ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
   } else {
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2;
@@ -643,17 +925,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // the dropout counter's head word: the call's head_base + the flattened head
     const uint32_t ctr_head = p.drop.head_base + static_cast<uint32_t>(bh);
-    RowScore rs{};
-    if constexpr (kScore != 0) {
-      const Span ks = keys_of_query(docs, prefix, p.score.n_docs, p.N, wl, wr, row);
-      rs.k_lo = ks.lo;
-      rs.k_hi = ks.hi;
-      // rows behind N are not written: they ask for no element tests
-      rs.full_lo = __reduce_max_sync(0xffffffffu, row < p.N ? ks.lo : 0);
-      rs.full_hi = __reduce_min_sync(0xffffffffu, row < p.N ? ks.hi : p.N);
-      if constexpr ((kScore & kScoreBias) != 0)
-        rs.slope_neg = -p.score.slopes[bh % p.score.H] * p.score.slope_mul;
-    }
     bool ok = t_nk > 0;
     int kt = t_lo - 1;
     for (int j = 0; j < t_nk && ok; ++j) {
@@ -663,10 +934,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (wq == 0) FA_TRACE_POINT(51, j, t);
       if (j == 0 && t == 0 && threadIdx.x == 0) FA_TRACE_CTA(2);
       if (!ok) break;
-      if (!softmax_key_tile<D, E, kDropout, kScore>(
-              p, wd, tm_s, tm_o, p_row, bar(C::kBarSFree + t), bar(C::kBarPVDone + t),
-              bar(C::kBarPFull + t), j, j == 0, kt, r0, row, row_in_tile, wl, wr, ctr_head, lane,
-              wq, t, m_ref, l, lr, rs)) {
+      if (!softmax_key_tile<D, E, kDropout>(p, wd, tm_s, tm_o, p_row, bar(C::kBarSFree + t),
+                                            bar(C::kBarPVDone + t), bar(C::kBarPFull + t), j,
+                                            j == 0, kt, r0, row, row_in_tile, wl,
+                                            wr, ctr_head, lane, wq, t, m_ref, l, lr)) {
         ok = false;
         break;
       }
@@ -1051,8 +1322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!softmax_key_tile<D, E, kDropout>(p, wd, tm_s, tm_o, p_row, bar(C::kBarSFree + t),
                                               bar(C::kBarPVDone + t), bar(C::kBarPFull + t),
                                               n, j == 0, kt, r0, row, row_in_tile,
-                                              wl, wr, ctr_head, lane, wq, t, m_ref, l, lr,
-                                              RowScore{})) {
+                                              wl, wr, ctr_head, lane, wq, t, m_ref, l, lr)) {
           ok = false;
           break;
         }

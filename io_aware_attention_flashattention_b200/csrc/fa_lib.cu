@@ -891,11 +891,11 @@ fa_status backward_impl(const void* Q, const void* K, const void* V, const void*
 
 // ---------------------------------------------------------------- shaped scores
 
-// softcap 0: none. The polynomial of tanh (see kTanhQ) takes the powers of a = scale / cap
-// into its coefficients, up to a^9, which must stay normal numbers: for a >= 2^-13 it is
-// used up to |x| = 0.7; below, its Taylor form of three terms up to |x| = 0.05, where the
-// next term is 8e-10 of the result. 1 - 2 / (1 + e^2x) takes over above, where its absolute
-// error of about 2e-7 is small next to x. So a is held to [2^-24, 2^12].
+// softcap 0: none. The polynomial of tanh (see kTanhQ5) takes the powers of a = scale / cap
+// into its coefficients, up to a^9, which must stay normal numbers: for a >= 2^-13 it is used
+// up to |x| = 0.8; below, its Taylor form of three terms up to |x| = 0.05, where the next
+// term is 8e-10 of the result. 1 - 2 / (1 + e^2x) takes over above, where its absolute
+// error of 6.3e-7 is small next to x. So a is held to [2^-24, 2^12].
 fa_status make_score(int B, int H, int Hkv, float scale, float softcap, const float* slopes,
                      const int32_t* documents, int n_docs, const int32_t* prefix,
                      ScoreParams* s) {
@@ -919,11 +919,15 @@ fa_status make_score(int B, int H, int Hkv, float scale, float softcap, const fl
     if (!(a >= 1.0 / (1 << 24) && a <= 4096.0)) return FA_ERR_UNSUPPORTED;
     const bool full = a >= 1.0 / 8192;
     const double taylor[5] = {1.0, -1.0 / 3, 2.0 / 15, 0.0, 0.0};
+    const double c = static_cast<double>(softcap) * 1.4426950408889634;
     double pw = a;
-    for (int k = 0; k < 5; ++k, pw *= a * a)
-      s->q[k] = static_cast<float>((full ? kTanhQ[k] : taylor[k]) * pw);
-    const double lim = (full ? static_cast<double>(kTanhLimit) : 0.05) / a;
-    s->lim2 = static_cast<float>(lim * lim);
+    for (int k = 0; k < 5; ++k, pw *= a * a) {
+      const double q5 = (full ? kTanhQ5[k] : taylor[k]) * pw;
+      s->q5[k] = static_cast<float>(q5);
+      s->cq5[k] = static_cast<float>(q5 * c);
+    }
+    const double lim5 = (full ? kTanhLimit5 : 0.05) / a;
+    s->lim5 = static_cast<float>(lim5 * lim5);
     s->cap_in2 = static_cast<float>(2.0 * 1.4426950408889634 * a);
   }
   s->slope_mul = softcap > 0.0f ? 1.0f / softcap : 1.0f / scale;
@@ -942,7 +946,7 @@ float score_log2(float scale, float softcap) {
 template <Elt E, int kScore>
 fa_status launch_fwd_scored(int d, unsigned grid, cudaStream_t s, const CUtensorMap& mq,
                             const CUtensorMap& mk, const CUtensorMap& mv, const fwd::Params& p) {
-  constexpr int T = fwd::kThreads;
+  constexpr int T = fwd::kThreadsScore;
   if (d == 64)
     return launch(fwd::fa_fwd_kernel<64, E, true, false, kScore>, grid, T,
                   fwd::Cfg<64>::kSmemBytes, s, mq, mk, mv, p);
@@ -1050,7 +1054,7 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
   pre.wr = mask.wr;
   pre.total_rows = static_cast<long long>(pl.BH) * pl.Npad;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned pre_blocks = static_cast<unsigned>((pre.total_rows + 7) / 8);
+  const unsigned pre_blocks = static_cast<unsigned>((pre.total_rows + 63) / 64);
   st = d == 64 ? launch(bwd::fa_bwd_pre_scored_kernel<64, E>, pre_blocks, 256, 0, s, pre)
                : launch(bwd::fa_bwd_pre_scored_kernel<128, E>, pre_blocks, 256, 0, s, pre);
   if (st != FA_OK) return st;

@@ -27,19 +27,20 @@ struct ScoreParams {
   int n_docs;           // >= 1
   int H;                // query heads per batch entry
   int group;            // query heads that share a K/V head
-  // tanh(x) = s * q(s^2) with x = s * scale / cap: q's coefficients with the powers of
-  // scale / cap folded in, and the bound on s^2 up to which it holds (see make_score)
-  float q[5];
-  float lim2;
-  float cap_in2;      // 2 * log2(e) * scale / cap, for the form on the exponential
+  // tanh(x) = s * q(s^2) with x = s * scale / cap: the polynomial's coefficients with the
+  // powers of scale / cap folded in, the same times c (what turns a tanh to a score in log2
+  // units), and the bound on s^2 up to which it holds (see make_score)
+  float q5[5], cq5[5];
+  float lim5;
+  float cap_in2;      // 2 * log2(e) * scale / cap, for the form on the exponential; 0: no cap
   float slope_mul;    // a slope times this is in units of the scores before c (below)
 };
 
-// tanh(x) / x as a polynomial in x^2 on |x| <= 0.7: least squares at Chebyshev nodes with
-// Lawson reweighting toward the minimax fit; largest relative error 3.1e-7.
-constexpr float kTanhLimit = 0.7f;
-constexpr double kTanhQ[5] = {0.9999996973, -0.3333021293, 0.1328111269, -0.05083623683,
-                              0.01377370979};
+// tanh(x) / x as a polynomial in x^2 for |x| <= 0.8: least squares at Chebyshev nodes with
+// Lawson reweighting toward the minimax fit; largest relative error 1.0e-6.
+constexpr double kTanhLimit5 = 0.8;
+constexpr double kTanhQ5[5] = {0.9999989944, -0.3332537202, 0.1323056571, -0.04918014249,
+                               0.01210013727};
 
 struct Span {
   int lo, hi;
@@ -144,18 +145,26 @@ __host__ __device__ __forceinline__ Span query_tiles_of_keys(const int* docs, co
   return Span{a.lo / 128, (b.hi + 127) / 128};
 }
 
-// tanh of a pair of scores on the FMA pipe, for s^2 <= lim2 (given as S = s * s).
-__device__ __forceinline__ float2 tanh_poly2(float2 s, float2 S, const ScoreParams& p) {
-  float2 r = ffma2(S, make_float2(p.q[4], p.q[4]), make_float2(p.q[3], p.q[3]));
-  r = ffma2(r, S, make_float2(p.q[2], p.q[2]));
-  r = ffma2(r, S, make_float2(p.q[1], p.q[1]));
-  r = ffma2(r, S, make_float2(p.q[0], p.q[0]));
-  return fmul2(s, r);
+// s * q(S) for a pair of scores, on the FMA pipe, with S = s * s.
+template <int n>
+__device__ __forceinline__ float2 odd_poly2(float2 S, const float (&q)[n]) {
+  float2 r = make_float2(q[n - 1], q[n - 1]);
+#pragma unroll
+  for (int k = n - 2; k >= 0; --k) r = ffma2(r, S, make_float2(q[k], q[k]));
+  return r;
+}
+template <int n>
+__device__ __forceinline__ float odd_poly(float s, const float (&q)[n]) {
+  const float S = s * s;
+  float r = q[n - 1];
+#pragma unroll
+  for (int k = n - 2; k >= 0; --k) r = fmaf(r, S, q[k]);
+  return s * r;
 }
 
 // tanh of one score of any size: 1 - 2 / (1 + e^2x), by the exponential and the reciprocal
-// of the MUFU unit. Absolute error about 2e-7, which the cap multiplies: fit for |x| of the
-// order of one and more, where the polynomial does not reach.
+// of the MUFU unit. Absolute error up to 6.3e-7, which the cap multiplies: fit for |x| of the
+// order of one and more, where the polynomials do not reach.
 __device__ __forceinline__ float tanh_exp(float s, float cap_in2) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(s * cap_in2)));
@@ -166,7 +175,7 @@ __device__ __forceinline__ float tanh_exp(float s, float cap_in2) {
 // (the branch would diverge otherwise): the polynomial where every score of the warp's
 // piece lies within its reach. Capped models keep most scores well inside the cap.
 template <int n>
-__device__ __forceinline__ void tanh_scores(uint32_t (&s)[n], const ScoreParams& p) {
+__device__ __forceinline__ void tanh_scores(uint32_t* s, const ScoreParams& p) {
   float2 S[n / 2];
   float top = 0.0f;
 #pragma unroll
@@ -175,31 +184,60 @@ __device__ __forceinline__ void tanh_scores(uint32_t (&s)[n], const ScoreParams&
     S[k] = fmul2(x, x);
     top = fmax3(top, S[k].x, S[k].y);
   }
-  if (__any_sync(0xffffffffu, !(top <= p.lim2))) {
+  if (__any_sync(0xffffffffu, !(top <= p.lim5))) {
 #pragma unroll
     for (int k = 0; k < n; ++k)
       s[k] = __float_as_uint(tanh_exp(__uint_as_float(s[k]), p.cap_in2));
   } else {
 #pragma unroll
     for (int k = 0; k < n / 2; ++k) {
-      const float2 r = tanh_poly2(
-          make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), S[k], p);
+      const float2 r =
+          fmul2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])),
+                odd_poly2(S[k], p.q5));
       s[2 * k] = __float_as_uint(r.x);
       s[2 * k + 1] = __float_as_uint(r.y);
     }
   }
 }
 
-// Subtracts the distance bias in place from n scores of consecutive columns: score k gets
-// slope_neg * |d0 + k| added, d0 the (whole) distance of column 0 from this thread's row.
-// Distances below 2^24 are exact in 32 bits.
+// Bits [lo, hi) of a word (any lo and hi), the visible columns of 32: one test of a constant
+// bit per score instead of an addition and a comparison. (shl by 32 or more gives 0.)
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi) {
+  uint32_t a, b;
+  asm("shl.b32 %0, %1, %2;" : "=r"(a) : "r"(0xffffffffu), "r"(max(lo, 0)));
+  asm("shl.b32 %0, %1, %2;" : "=r"(b) : "r"(0xffffffffu), "r"(max(hi, 0)));
+  return a & ~b;
+}
+
+// Adds slope_neg * |d0 + k| to n scores of consecutive columns k, in place; d0 is the (whole)
+// distance of column 0 from this thread's row. Where all distances of the warp have one sign
+// the bias runs in pairs, from an exact start every 16 columns (distances below 2^24 are
+// exact in 32 bits) by at most seven additions.
 template <int n>
 __device__ __forceinline__ void bias_scores(uint32_t (&s)[n], int d0, float slope_neg) {
-  const float f0 = static_cast<float>(d0);
+  const bool right = d0 >= 0, left = d0 + n - 1 <= 0;
+  if (__all_sync(0xffffffffu, right) || __all_sync(0xffffffffu, left)) {
+    const float sl = right ? slope_neg : -slope_neg;
 #pragma unroll
-  for (int k = 0; k < n; ++k)
-    s[k] = __float_as_uint(
-        fmaf(slope_neg, fabsf(f0 + static_cast<float>(k)), __uint_as_float(s[k])));
+    for (int k = 0; k < n; k += 16) {
+      const float f = static_cast<float>(d0 + k) * sl;
+      float2 b = make_float2(f, f + sl);
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float2 x = fadd2(b, make_float2(__uint_as_float(s[k + e]),
+                                              __uint_as_float(s[k + e + 1])));
+        s[k + e] = __float_as_uint(x.x);
+        s[k + e + 1] = __float_as_uint(x.y);
+        b = fadd2(b, make_float2(2.0f * sl, 2.0f * sl));
+      }
+    }
+  } else {
+    const float f0 = static_cast<float>(d0);
+#pragma unroll
+    for (int k = 0; k < n; ++k)
+      s[k] = __float_as_uint(
+          fmaf(slope_neg, fabsf(f0 + static_cast<float>(k)), __uint_as_float(s[k])));
+  }
 }
 
 }  // namespace fa

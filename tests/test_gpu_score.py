@@ -135,16 +135,18 @@ def test_documents_match_separate_calls_bit_for_bit_in_the_forward():
 
 
 def test_off_terms_give_the_plain_calls_results():
-    """No cap, one document, no prefix: bit for bit the plain forward, and dV; dK of the keys
-    that only queries of more than 16 keys see (the others' D is formed more exactly)."""
+    """No cap, one document, no prefix: the plain calls' results, both within the bounds (the
+    kernels sum in another order), and dV, whose weights both form alike, bit for bit."""
     q, k, v, do = make(2, 3, 3, 300, 64, HF, seed=9)
     one = torch.tensor([[0, 300]] * 2, dtype=torch.int32, device="cuda")
+    mask = ref.visible(2, 300, True)
     o, lse = api.forward(q, k, v, causal=True, documents=one)
-    a, b = api.forward(q, k, v, causal=True)
-    assert torch.equal(o, a) and torch.equal(lse, b)
     got = api.backward(q, k, v, o, lse, do, causal=True, documents=one)
+    check((o, lse) + got, q, k, v, do, mask, 0.125, None, None)
     want = api.backward(q, k, v, o, lse, do, causal=True)
-    assert torch.equal(got[1][:, :, 16:], want[1][:, :, 16:]) and torch.equal(got[2], want[2])
+    assert torch.equal(got[2], want[2])
+    o, lse = api.forward(q, k, v, causal=True)
+    check((o, lse) + api.backward(q, k, v, o, lse, do, causal=True), q, k, v, do, mask, 0.125, None, None)
 
 
 @pytest.mark.parametrize("window", [(40, -1), (3, 2)])
