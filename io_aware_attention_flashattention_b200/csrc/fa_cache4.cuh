@@ -61,14 +61,21 @@ struct Divisor {
   }
 };
 
+// (w & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  return r;
+}
+
 // ------------------------------------------------------------------ append and read
 //
 // A row by D / 16 neighbouring lanes, 16 channels (32 bytes, 8 bytes of codes) each. The
 // kernels move 2 D + D / 2 + 4 bytes per row and are bound by memory as long as a thread
 // spends few enough instructions on its 16 channels: row indices by products instead of
 // divisions, the quotient by a reciprocal (see quantise), codes to floats by the mantissa.
-// B16 Hkv8 n2048 ragged d128 (260 MB both ways) with IEEE divisions for each: 95 us for
-// the append and 58 us for the read.
+// B16 Hkv8 n2048 ragged d128 (130 MB each): the append 95 us with a division for each value,
+// 58 us with one for those near a half, @P@; the read 58 us, then 37 us, @Q@.
 
 struct RowsParams {
   uint16_t* K;  // read by the append, written by the read
@@ -124,36 +131,46 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-// code = round((x - lo) / scale), halves to even, of the quotient rounded to 32 bits. The
-// product with the reciprocal lies within 3 roundings (3e-6 at 15) of that quotient, so it
-// rounds to the same code unless it comes within 1e-5 of a half: then, and where the scale
-// is below the type's normal numbers (codes may pass 15) or x - lo passes 32 bits, the
-// quotient itself is formed. Adding 1.5 * 2^23 rounds and leaves the code in the low bits.
+// Codes round((x - lo) / scale), halves to even, of 16 values given as 8 pairs. With inv the
+// correctly rounded reciprocal, q0 = d inv and r = d - q0 scale (exact), fma(r, inv, q0) is
+// the correctly rounded quotient (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990), in pairs and without a branch: ties are common among
+// 16-bit values, so a test for them sent most warps to a division each. Adding 1.5 * 2^23
+// rounds and leaves the code in the low bits; the sum of the shifted bits holds a constant
+// beside the codes. Where the scale is below the type's normal numbers (codes may pass 15, and
+// the products may leave the normal range) or x - lo passes 32 bits the quotients are formed
+// one by one.
 template <Elt E>
-__device__ __forceinline__ uint2 quantise(const float (&x)[16], float lo, float hi, float scale) {
+__device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], float lo, float hi, float scale) {
   constexpr float kMagic = 12582912.0f;
-  constexpr float kNormal = E == Elt::BF16 ? 1e-36f : 6.2e-5f;
-  const float inv = __frcp_rn(scale);
-  float worst = 0.0f;
+  constexpr float kNormal = E == Elt::BF16 ? 1e-30f : 6.2e-5f;
   uint32_t code[2] = {0u, 0u};
+  if (scale >= kNormal && hi - lo < 3.0e38f) {
+    const float inv = __frcp_rn(scale);
+    const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-scale, -scale);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const float d = x[k] - lo;
-    const float y = fmaf(d, inv, kMagic);
-    worst = fmaxf(worst, fabsf(fmaf(d, inv, -(y - kMagic))));
-    code[k / 8] += (__float_as_uint(y) & 15u) << (4 * (k % 8));
-  }
-  if (!(worst < 0.49999f) || !(scale >= kNormal) || !(hi - lo < 3.0e38f)) {
-    code[0] = code[1] = 0u;
-    if (scale > 0.0f) {
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h)
+    for (int k = 0; k < 8; ++k) {
+      const float2 d = fadd2(unpack2<E>(w[k]), make_float2(-lo, -lo));
+      const float2 q0 = fmul2(d, inv2);
+      const float2 q = ffma2(ffma2(q0, neg2, d), inv2, q0);
+      const float2 y = fadd2(q, make_float2(kMagic, kMagic));
+      code[k / 4] += (__float_as_uint(y.x) << (8 * (k % 4))) +
+                     (__float_as_uint(y.y) << (8 * (k % 4) + 4));
+    }
+    // the sum of 0x4B400000 << 4k over k = 0..7, modulo 2^32
+    constexpr uint32_t kConstant = 0x4B400000u + (0x4B400000u << 4) + (0x4B400000u << 8) +
+                                   (0x4B400000u << 12) + (0x4B400000u << 16) +
+                                   (0x4B400000u << 20) + (0x4B400000u << 24) +
+                                   (0x4B400000u << 28);
+    code[0] -= kConstant;
+    code[1] -= kConstant;
+  } else if (scale > 0.0f) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float v = h ? x[8 + k] : x[k];
-          const float c = fminf(fmaxf(rintf(__fdiv_rn(v - lo, scale)), 0.0f), 15.0f);
-          code[h] |= static_cast<uint32_t>(c) << (4 * k);
-        }
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = unpack2<E>(w[k / 2]);
+      const float c =
+          fminf(fmaxf(rintf(__fdiv_rn(((k & 1) ? x.y : x.x) - lo, scale)), 0.0f), 15.0f);
+      code[k / 8] |= static_cast<uint32_t>(c) << (4 * (k % 8));
     }
   }
   return make_uint2(code[0], code[1]);
@@ -189,14 +206,7 @@ __global__ void __launch_bounds__(256) append_kernel(const RowsParams p) {
   // by itself: their difference may pass the largest bf16.
   constexpr float kFifteenth = 1.0f / 15.0f;
   const uint32_t sz = pack2<E>(__fsub_rn(__fmul_rn(hi, kFifteenth), __fmul_rn(lo, kFifteenth)), lo);
-  float x[16];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float2 f = unpack2<E>(w[k]);
-    x[2 * k] = f.x;
-    x[2 * k + 1] = f.y;
-  }
-  const uint2 code = quantise<E>(x, lo, hi, scale_zero<E>(sz).x);
+  const uint2 code = quantise<E>(w, lo, hi, scale_zero<E>(sz).x);
   reinterpret_cast<uint2*>(p.L.codes + a.row * (D / 2))[a.lane] = code;
   if (a.lane == 0) p.L.params[a.row] = sz;
 }
@@ -212,14 +222,16 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
   if (a.row >= 0) {
     const uint2 code = reinterpret_cast<const uint2*>(p.L.codes + a.row * (D / 2))[a.lane];
     const float2 sz = scale_zero<E>(p.L.params[a.row]);
-    // 2^23 + code, less 2^23
-    auto value = [&](uint32_t c, int k) {
-      return fmaf(sz.x, __uint_as_float(((c >> (4 * k)) & 15u) | 0x4B000000u) - 8388608.0f, sz.y);
-    };
+    const float2 s2 = make_float2(sz.x, sz.x), z2 = make_float2(sz.y, sz.y);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      o[k] = pack2<E>(value(code.x, 2 * k), value(code.x, 2 * k + 1));
-      o[4 + k] = pack2<E>(value(code.y, 2 * k), value(code.y, 2 * k + 1));
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t c = (k < 4 ? code.x : code.y) >> (8 * (k % 4));
+      // 2^23 + code, less 2^23
+      const float2 v = fadd2(make_float2(__uint_as_float(and_or(c, 15u, 0x4B000000u)),
+                                         __uint_as_float(and_or(c >> 4, 15u, 0x4B000000u))),
+                             make_float2(-8388608.0f, -8388608.0f));
+      const float2 x = ffma2(s2, v, z2);
+      o[k] = pack2<E>(x.x, x.y);
     }
   }
   uint4* dst = reinterpret_cast<uint4*>((a.which ? p.V : p.K) + static_cast<size_t>(a.r) * D) +
@@ -232,22 +244,22 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
 //
 // One CTA of kWarps warps takes one K/V head of one sequence, up to 8 * NT query rows (the
 // group's heads times the draft's tokens) and a piece of the sequence; every warp takes
-// every kWarps-th group of 16 tokens of it and keeps its own running maximum, sum and
+// every kWarps-th step of 32 tokens of it and keeps its own running maximum, sum and
 // output, joined at the end over the warps and then (by combine_kernel) over the pieces.
 // Products on the tensor cores (mma.m16n8k16, fp32 accumulators) with tokens, then
 // channels, as the 16 rows, so that up to 8 query rows cost one product:
 //   S^T[16 tokens x 8 rows] = codes[16 x d] Q^T[d x 8]
 //   O^T[d x 8] += V codes^T[d x 16] P^T[16 x 8]
-// A group's codes and pairs (2 * 8 d + 128 bytes) come through a ring of shared memory of
-// the warp's own, kStages - 1 groups ahead by asynchronous copies, and leave it in the order
+// A step's codes and pairs (32 (d + 8) bytes) come through two buffers of shared memory of
+// the warp's own, one step ahead by asynchronous copies, and leave them in the order
 // that the products take them: a thread reads whole words of 8 codes, and any order of the
 // summed index will do as long as both operands follow it. Two codes of a word become a
-// pair of 16-bit floats 128 + code (bf16) or 1024 + code (f16) by a shift and one logical
-// operation, the code being the last bits of the mantissa, and c - 8 by one packed addition
-// (exact). With sum q = qs:
+// pair of 16-bit floats c - 8 by a shift, one logical operation and one packed addition. (16 +
+// c would save K the addition, at the price of a shift: no faster, and less exact.) With
+// sum q = qs:
 //   s = scale_k * (sum q (c - 8)) + (zero_k + 8 scale_k) qs
 // and, with P' = P scale_v:
-//   o = sum P' (c - 8) + sum (P zero_v + 8 P').
+//   o = sum P' (c - 8) + sum P (zero_v + 8 scale_v).
 // P' enters its product as a sum of two bf16, P' rounded and what that leaves (2^-17 of P'
 // is lost): one bf16 alone put the output 2.4e-3 off in f16 (B1 H32 Hkv4 L131071 d128),
 // ten times that type's own rounding. f16 would not do: scales times weights of long rows
@@ -257,8 +269,8 @@ __global__ void __launch_bounds__(256) read_kernel(const RowsParams p) {
 // unpack codes: shifts and logical operations issue at half rate.
 
 constexpr int kWarps = 4;
-constexpr int kGroup = 16;  // tokens per step of a warp
-constexpr int kStages = 4;
+constexpr int kGroup = 16;  // tokens of one product: the rows that a page holds whole
+constexpr int kStep = 32;   // tokens per step of a warp: two groups
 
 struct AttendParams {
   const uint16_t* Q;  // [B, H, Nq, D]
@@ -271,9 +283,10 @@ struct AttendParams {
   ScoreParams score;
   int B, H, Nq;
   int rows;      // query rows per K/V head: group * Nq
+  Divisor nq;
   int row_tiles;  // CTAs they take
   int n_pieces;
-  int piece;  // groups per piece, a multiple of kWarps
+  int piece;  // steps per piece, a multiple of kWarps
   int wl;     // < 0: no window
   float scale_log2;
 };
@@ -302,16 +315,17 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-// Nibbles j of both halves of a word as a pair of 16-bit floats code - 8.
+// Nibbles j of both halves of a word as a pair of 16-bit floats code - 8: 128 + code (bf16) or
+// 1024 + code (f16), the code being the mantissa's last bits, and one exact addition.
 template <Elt E, int j>
 __device__ __forceinline__ uint32_t centred(uint32_t w) {
   uint32_t r;
   if constexpr (E == Elt::BF16)
     asm("add.rn.bf16x2 %0, %1, %2;"
-        : "=r"(r) : "r"(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u), "r"(0xC308C308u));
+        : "=r"(r) : "r"(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u)), "r"(0xC308C308u));
   else
     asm("add.rn.f16x2 %0, %1, %2;"
-        : "=r"(r) : "r"(((w >> (4 * j)) & 0x000F000Fu) | 0x64006400u), "r"(0xE408E408u));
+        : "=r"(r) : "r"(and_or(w >> (4 * j), 0x000F000Fu, 0x64006400u)), "r"(0xE408E408u));
   return r;
 }
 
@@ -350,12 +364,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   constexpr int R = 8 * NT;      // query rows of the CTA
   constexpr int KS = D / 16;     // steps of the score product
   constexpr int MT = D / 16;     // 16-channel blocks of the output
-  constexpr int kRow = D / 2;    // bytes of a row's codes
+  constexpr int kRow = D / 2;               // bytes of a row's codes
   constexpr int kHalf = kGroup * kRow;      // of a group's K or V codes
-  constexpr int kStage = 2 * kHalf + 2 * kGroup * 4;
-  constexpr int kRing = kWarps * kStages * kStage;
+  constexpr int kPart = 2 * kHalf + 2 * kGroup * 4;  // of a group: codes, then the pairs
+  constexpr int kRing = kWarps * 4 * kPart;
   constexpr int kJoin = kWarps * R * (D + 4 + 2) * 4;
-  // the ring, and after the loop the warps' results
+  // the buffers, and after the loop the warps' results
   __shared__ __align__(128) uint8_t smem[kRing > kJoin ? kRing : kJoin];
   float (*const sm_o)[R][D + 4] = reinterpret_cast<float (*)[R][D + 4]>(smem);
   float (*const sm_m)[R] = reinterpret_cast<float (*)[R]>(smem + kWarps * R * (D + 4) * 4);
@@ -373,9 +387,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int row0 = rt * R;
   const int n_rows = min(R, p.rows - row0);
   const int group = p.score.group;
-  // the row of [B, H, Nq] that row r of this K/V head is
+  // row r of this K/V head: its head of the group and its token of the draft, and its row of
+  // [B, H, Nq]
+  auto head_of = [&](int r) -> int { return static_cast<int>(p.nq.quotient(r)); };
   auto out_row = [&](int r) -> size_t {
-    return (static_cast<size_t>(b) * p.H + hk * group + r / p.Nq) * p.Nq + r % p.Nq;
+    const int h = head_of(r);
+    return (static_cast<size_t>(b) * p.H + hk * group + h) * p.Nq + (r - h * p.Nq);
   };
 
   const long long room = static_cast<long long>(p.L.max_pages) << p.L.shift;
@@ -386,10 +403,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   const int pos0 = len - p.Nq;  // of the draft's first token
   const int first = p.wl < 0 ? 0 : max(0, pos0 - p.wl);
-  const int g_lo = first / kGroup, g_hi = (len + kGroup - 1) / kGroup;
+  const int g_hi = (len + kGroup - 1) / kGroup;                    // groups with tokens
+  const int s_lo = first / kStep, s_hi = (len + kStep - 1) / kStep;  // steps
   const int* table = p.L.table + static_cast<size_t>(b) * p.L.max_pages;
 
-  // this warp's groups: g_lo + piece * p.piece + warp, every kWarps-th of the piece, then the
+  // this warp's steps: s_lo + piece * p.piece + warp, every kWarps-th of the piece, then the
   // same of piece + n_pieces, ... (more than one only where a length passes the given bound)
   auto next = [&](int x, int& in) -> int {
     in += kWarps;
@@ -401,48 +419,56 @@ __global__ void __launch_bounds__(kWarps * 32)
     return x;
   };
 
-  // Copies of one group into a stage: a thread's units of the K and V codes (unit lane of
-  // each 512 bytes) and one of the 32 pairs. A group without a page takes page 0 instead (the
-  // reads stay inside the cache) and is marked.
-  const uint32_t ring = smem_u32(smem) + warp * (kStages * kStage);
+  // Copies of one group into part 2 * buffer + (0, 1) of the warp's ring: a thread's units of
+  // the K and V codes (unit lane of each 512 bytes) and one of the 32 pairs. A group without
+  // a page takes page 0 instead (the reads stay inside the cache) and is marked.
+  const uint32_t ring = smem_u32(smem) + warp * (4 * kPart);
   const unsigned page_groups = p.L.shift - 4;  // log2 of the groups per page
   const unsigned n_pages = static_cast<unsigned>(p.L.n_pages);
+  const unsigned heads2 = 2 * p.L.Hkv, slots = p.L.page - 1;
   const size_t v_rows = static_cast<size_t>(p.L.Hkv) << p.L.shift;  // from K's rows to V's
   constexpr int kUnits = kHalf / 512;  // copies of a thread per half: 2 (D = 128) or 1
   constexpr int kPerRow = D / 32;      // units of a row
-  unsigned bad = 0;                    // stages whose group has no page
-  auto issue = [&](int x, int stage) {
-    if (x < g_hi) {
-      unsigned id = static_cast<unsigned>(__ldg(table + (x >> page_groups)));
-      bad &= ~(1u << stage);
-      if (id >= n_pages) {
-        bad |= 1u << stage;
-        id = 0;
-      }
-      const size_t row = (static_cast<size_t>(id) * (2 * p.L.Hkv) + hk << p.L.shift) +
-                         ((x << 4) & (p.L.page - 1));
-      const uint8_t* k = p.L.codes + row * kRow + lane * 16;
-      const uint8_t* v = k + v_rows * kRow;
-      const uint32_t dst = ring + stage * kStage;
+  const uint8_t* const codes_lane = p.L.codes + lane * 16;
+  const uint32_t* const params_lane = p.L.params + (lane & 15) + (lane < 16 ? 0 : v_rows);
+  uint32_t dst_k[kUnits], dst_v[kUnits];
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const int unit = u * 32 + lane;
-        copy_async(dst + ring_unit<D>(0, unit / kPerRow, unit % kPerRow) * 16, k + u * 512, true);
-        copy_async(dst + kHalf + ring_unit<D>(1, unit / kPerRow, unit % kPerRow) * 16, v + u * 512,
-                   true);
+  for (int u = 0; u < kUnits; ++u) {
+    const int unit = u * 32 + lane;
+    dst_k[u] = ring + ring_unit<D>(0, unit / kPerRow, unit % kPerRow) * 16;
+    dst_v[u] = ring + kHalf + ring_unit<D>(1, unit / kPerRow, unit % kPerRow) * 16;
+  }
+  unsigned bad = 0;  // parts whose group has no page
+  auto issue = [&](int x, int buffer) {  // the step x
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const int grp = 2 * x + part, slot = 2 * buffer + part;
+      if (grp < g_hi) {
+        unsigned id = static_cast<unsigned>(__ldg(table + (grp >> page_groups)));
+        bad &= ~(1u << slot);
+        if (id >= n_pages) {
+          bad |= 1u << slot;
+          id = 0;
+        }
+        const size_t row = ((static_cast<size_t>(id) * heads2 + hk) << p.L.shift) +
+                           ((grp << 4) & slots);
+        const uint8_t* k = codes_lane + row * kRow;
+        const uint8_t* v = k + v_rows * kRow;
+        const uint32_t off = slot * kPart;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          copy_async(dst_k[u] + off, k + u * 512, true);
+          copy_async(dst_v[u] + off, v + u * 512, true);
+        }
+        copy_async(ring + 2 * kHalf + lane * 4 + off, params_lane + row, false);
       }
-      copy_async(dst + 2 * kHalf + lane * 4,
-                 p.L.params + row + (lane & 15) + (lane < 16 ? 0 : v_rows), false);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  int use = g_lo + piece * p.piece + warp, use_in = 0;
+  int use = s_lo + piece * p.piece + warp, use_in = 0;
   int ahead = use, ahead_in = 0;
-#pragma unroll
-  for (int k = 0; k < kStages - 1; ++k) {
-    issue(ahead, k);
-    ahead = next(ahead, ahead_in);
-  }
+  issue(ahead, 0);
+  ahead = next(ahead, ahead_in);
 
   // the queries, as the score product's second operand, and the sums of their channels
   uint32_t q[NT][KS][2];
@@ -476,23 +502,25 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = min(row0 + nt * 8 + 2 * t + e, p.rows - 1);
-      pos[nt][e] = pos0 + r % p.Nq;
+      const int r = min(row0 + nt * 8 + 2 * t + e, p.rows - 1), h = head_of(r);
+      pos[nt][e] = pos0 + (r - h * p.Nq);
       if constexpr ((kMods & kScoreBias) != 0)
         slope_neg[nt][e] =
-            -__ldg(p.score.slopes + hk * group + r / p.Nq) * p.score.slope_mul * p.scale_log2;
+            -__ldg(p.score.slopes + hk * group + h) * p.score.slope_mul * p.scale_log2;
     }
 
   // Without a cap the scores are in log2 units from the start: c goes into scale and zero.
   const float c = p.scale_log2;
   const float c_in = (kMods & kScoreCap) ? 1.0f : c;
-  float m[NT][2], l[NT][2], z[NT][2], o[NT][MT][4];
+  // m: the reference maximum (0 before there is one: bound is -inf then); bound: where a
+  // score moves it; l, z: this thread's parts of the sums of P and of P (zero_v + 8 scale_v)
+  float m[NT][2], bound[NT][2], l[NT][2], z[NT][2], o[NT][MT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      m[nt][e] = -INFINITY;
-      l[nt][e] = z[nt][e] = 0.0f;
+      bound[nt][e] = -INFINITY;
+      m[nt][e] = l[nt][e] = z[nt][e] = 0.0f;
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -501,169 +529,183 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   const int own = (g >> 1) + (g & 1) * 4;  // the token of the products' row g; g + 8: own + 8
   const int edge_hi = pos0 - kGroup + 1, edge_lo = p.wl < 0 ? -1 : len - 1 - p.wl;
+  // this thread's reads of a part
+  uint32_t src_k[2], src_v[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int byte = t * (D / 8);
+    src_k[h] = ring + ring_unit<D>(0, own + 8 * h, byte / 16) * 16 + byte % 16;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int byte = g * (D / 16);
+    src_v[i] = ring + kHalf + ring_unit<D>(1, 4 * i + t, byte / 16) * 16 + byte % 16;
+  }
+  const uint32_t src_p = ring + 2 * kHalf + own * 4;
 
-  for (int it = 0; use < g_hi; ++it) {
-    const int stage = it & (kStages - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    __syncwarp();  // every lane's copies are in, and every lane is done with the stage before
-    issue(ahead, (it + kStages - 1) & (kStages - 1));
+  for (int buffer = 0; use < s_hi; buffer ^= 1) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();  // every lane's copies are in, and every lane is done with the other buffer
+    issue(ahead, buffer ^ 1);
     ahead = next(ahead, ahead_in);
-    const int k0 = use * kGroup;
+    const int step = use;
     use = next(use, use_in);
-    if ((bad >> stage) & 1u) {  // tokens without a page are not there
-      if (lane == 0) atomicOr(&g_status, kStatusBadPage);
-      continue;
-    }
-    const uint32_t src = ring + stage * kStage;
-    // scores: (token own + 8h, row 2t + e) is s[nt][2h + e]
-    float s[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-    {
-      uint32_t k[2][D / 32];  // channels t * D / 4 on of the two tokens
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int byte = t * (D / 8);
-        shared_words(k[h], src + ring_unit<D>(0, own + 8 * h, byte / 16) * 16 + byte % 16);
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+      const int k0 = (2 * step + part) * kGroup, slot = 2 * buffer + part;
+      if (k0 >= len) break;
+      if ((bad >> slot) & 1u) {  // tokens without a page are not there
+        if (lane == 0) atomicOr(&g_status, kStatusBadPage);
+        continue;
       }
+      const uint32_t off = slot * kPart;
+      // scores: (token own + 8h, row 2t + e) is s[nt][2h + e]
+      float s[NT][4];
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        const uint32_t a0[4] = {centred<E, 0>(k[0][w]), centred<E, 0>(k[1][w]),
-                                centred<E, 1>(k[0][w]), centred<E, 1>(k[1][w])};
-        const uint32_t a1[4] = {centred<E, 2>(k[0][w]), centred<E, 2>(k[1][w]),
-                                centred<E, 3>(k[0][w]), centred<E, 3>(k[1][w])};
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_16n8k16<E>(s[nt], a0, q[nt][2 * w][0], q[nt][2 * w][1]);
-          mma_16n8k16<E>(s[nt], a1, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+      {
+        uint32_t k[2][D / 32];  // channels t * D / 4 on of the two tokens
+#pragma unroll
+        for (int h = 0; h < 2; ++h) shared_words(k[h], src_k[h] + off);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint32_t a0[4] = {centred<E, 0>(k[0][w]), centred<E, 0>(k[1][w]),
+                                  centred<E, 1>(k[0][w]), centred<E, 1>(k[1][w])};
+          const uint32_t a1[4] = {centred<E, 2>(k[0][w]), centred<E, 2>(k[1][w]),
+                                  centred<E, 3>(k[0][w]), centred<E, 3>(k[1][w])};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16n8k16<E>(s[nt], a0, q[nt][2 * w][0], q[nt][2 * w][1]);
+            mma_16n8k16<E>(s[nt], a1, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+          }
         }
       }
-    }
-    float2 ksz[2], vsz[2];
+      float2 ksz[2], vsz[2];  // scale, and zero + 8 scale
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w[1];
-      shared_words(w, src + 2 * kHalf + (own + 8 * h) * 4);
-      ksz[h] = unpack2<E>(w[0]);
-      ksz[h].x *= c_in;
-      ksz[h].y = fmaf(ksz[h].y, c_in, 8.0f * ksz[h].x);
-      shared_words(w, src + 2 * kHalf + (kGroup + own + 8 * h) * 4);
-      vsz[h] = unpack2<E>(w[0]);
-    }
-    uint32_t u[4 * NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        u[4 * nt + e] =
-            __float_as_uint(fmaf(ksz[e >> 1].x, s[nt][e], ksz[e >> 1].y * qs[nt][e & 1]));
-    if constexpr ((kMods & kScoreCap) != 0) {
-      tanh_scores<4 * NT>(u, p.score);
-#pragma unroll
-      for (int e = 0; e < 4 * NT; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * c);
-    }
-    if constexpr ((kMods & kScoreBias) != 0) {
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[1];
+        shared_words(w, src_p + off + 32 * h);
+        ksz[h] = unpack2<E>(w[0]);
+        ksz[h].y = fmaf(8.0f, ksz[h].x, ksz[h].y) * c_in;
+        ksz[h].x *= c_in;
+        shared_words(w, src_p + off + 64 + 32 * h);
+        vsz[h] = unpack2<E>(w[0]);
+        vsz[h].y = fmaf(8.0f, vsz[h].x, vsz[h].y);
+      }
+      uint32_t u[4 * NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          u[4 * nt + e] = __float_as_uint(
-              fmaf(slope_neg[nt][e & 1],
-                   static_cast<float>(pos[nt][e & 1] - (k0 + own + 8 * (e >> 1))),
-                   __uint_as_float(u[4 * nt + e])));
-    }
-    // rows' keys are [pos - wl, pos]: tests only where the 16 tokens cross an edge
-    if (k0 > edge_hi || k0 < edge_lo) {
+          u[4 * nt + e] =
+              __float_as_uint(fmaf(ksz[e >> 1].x, s[nt][e], ksz[e >> 1].y * qs[nt][e & 1]));
+      if constexpr ((kMods & kScoreCap) != 0) {
+        tanh_scores<4 * NT>(u, p.score);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = k0 + own + 8 * h;
+        for (int e = 0; e < 4 * NT; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * c);
+      }
+      if constexpr ((kMods & kScoreBias) != 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (key > pos[nt][e] || (p.wl >= 0 && key < pos[nt][e] - p.wl))
-              u[4 * nt + 2 * h + e] = __float_as_uint(-INFINITY);
-        // a token that no row sees has weight 0, whatever its slot holds
-        if (key >= len || (p.wl >= 0 && key < pos0 - p.wl)) vsz[h] = make_float2(0.0f, 0.0f);
+          for (int e = 0; e < 4; ++e)
+            u[4 * nt + e] = __float_as_uint(
+                fmaf(slope_neg[nt][e & 1],
+                     static_cast<float>(pos[nt][e & 1] - (k0 + own + 8 * (e >> 1))),
+                     __uint_as_float(u[4 * nt + e])));
       }
-    }
-    bool up = false;
+      // rows' keys are [pos - wl, pos]: tests only where the 16 tokens cross an edge
+      if (k0 > edge_hi || k0 < edge_lo) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < 2; ++h) {
+          const int key = k0 + own + 8 * h;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[nt][e] = __uint_as_float(u[4 * nt + e]);
-        up = up || s[nt][e] > m[nt][e & 1] + 8.0f;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (key > pos[nt][e] || (p.wl >= 0 && key < pos[nt][e] - p.wl))
+                u[4 * nt + 2 * h + e] = __float_as_uint(-INFINITY);
+          // a token that no row sees has weight 0, whatever its slot holds
+          if (key >= len || (p.wl >= 0 && key < pos0 - p.wl)) vsz[h] = make_float2(0.0f, 0.0f);
+        }
       }
-    if (__any_sync(0xffffffffu, up)) {
+      bool up = false;
+      float top[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float alpha[2];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(s[nt][e], s[nt][2 + e]);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const float now = fmaxf(m[nt][e], top);
-          alpha[e] = m[nt][e] == -INFINITY ? 0.0f : ex2_approx(m[nt][e] - now);
-          m[nt][e] = now;
-          l[nt][e] *= alpha[e];
-          z[nt][e] *= alpha[e];
+          s[nt][e] = __uint_as_float(u[4 * nt + e]);
+          s[nt][2 + e] = __uint_as_float(u[4 * nt + 2 + e]);
+          top[nt][e] = fmaxf(s[nt][e], s[nt][2 + e]);
+          up = up || top[nt][e] > bound[nt][e];
         }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
-      }
-    }
-    uint32_t pb[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float base = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
-        w[e] = ex2_approx(s[nt][e] - base);
-        l[nt][e & 1] += w[e];
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float a = w[2 * h] * vsz[h].x, b = w[2 * h + 1] * vsz[h].x;
-        const uint32_t pk = pack_bf16x2(a, b);
-        const float2 back = unpack2<Elt::BF16>(pk);
-        z[nt][0] = fmaf(8.0f, a, fmaf(w[2 * h], vsz[h].y, z[nt][0]));
-        z[nt][1] = fmaf(8.0f, b, fmaf(w[2 * h + 1], vsz[h].y, z[nt][1]));
-        pb[nt][h] = transpose8(pk);
-        pb[nt][2 + h] = transpose8(pack_bf16x2(a - back.x, b - back.y));
-      }
-    }
-    uint32_t v[4][D / 64];  // tokens t, 4 + t, 8 + t, 12 + t: channels g * D / 8 on
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int byte = g * (D / 16);
-      shared_words(v[i], src + kHalf + ring_unit<D>(1, 4 * i + t, byte / 16) * 16 + byte % 16);
-    }
-#pragma unroll
-    for (int w = 0; w < D / 64; ++w) {
-      constexpr Elt B = Elt::BF16;
-      const uint32_t lo0 = __byte_perm(v[0][w], v[1][w], 0x5410);
-      const uint32_t lo1 = __byte_perm(v[2][w], v[3][w], 0x5410);
-      const uint32_t hi0 = __byte_perm(v[0][w], v[1][w], 0x7632);
-      const uint32_t hi1 = __byte_perm(v[2][w], v[3][w], 0x7632);
-      const uint32_t a[4][4] = {
-          {centred<B, 0>(lo0), centred<B, 1>(lo0), centred<B, 0>(lo1), centred<B, 1>(lo1)},
-          {centred<B, 2>(lo0), centred<B, 3>(lo0), centred<B, 2>(lo1), centred<B, 3>(lo1)},
-          {centred<B, 0>(hi0), centred<B, 1>(hi0), centred<B, 0>(hi1), centred<B, 1>(hi1)},
-          {centred<B, 2>(hi0), centred<B, 3>(hi0), centred<B, 2>(hi1), centred<B, 3>(hi1)}};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
+      if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_16n8k16<B>(o[nt][4 * w + i], a[i], pb[nt][0], pb[nt][1]);
-          mma_16n8k16<B>(o[nt][4 * w + i], a[i], pb[nt][2], pb[nt][3]);
+          float alpha[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = top[nt][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            const float was = bound[nt][e] == -INFINITY ? -INFINITY : m[nt][e];
+            const float now = fmaxf(was, x);
+            alpha[e] = ex2_approx(was - (now == -INFINITY ? 0.0f : now));  // 0 at first
+            m[nt][e] = now == -INFINITY ? 0.0f : now;
+            bound[nt][e] = now + 8.0f;
+            l[nt][e] *= alpha[e];
+            z[nt][e] *= alpha[e];
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
         }
+      }
+      uint32_t pb[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = ex2_approx(s[nt][e] - m[nt][e & 1]);
+          l[nt][e & 1] += w[e];
+          z[nt][e & 1] = fmaf(w[e], vsz[e >> 1].y, z[nt][e & 1]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float a = w[2 * h] * vsz[h].x, b = w[2 * h + 1] * vsz[h].x;
+          const uint32_t pk = pack_bf16x2(a, b);
+          const float2 back = unpack2<Elt::BF16>(pk);
+          pb[nt][h] = transpose8(pk);
+          pb[nt][2 + h] = transpose8(pack_bf16x2(a - back.x, b - back.y));
+        }
+      }
+      uint32_t v[4][D / 64];  // tokens t, 4 + t, 8 + t, 12 + t: channels g * D / 8 on
+#pragma unroll
+      for (int i = 0; i < 4; ++i) shared_words(v[i], src_v[i] + off);
+#pragma unroll
+      for (int w = 0; w < D / 64; ++w) {
+        const uint32_t lo0 = __byte_perm(v[0][w], v[1][w], 0x5410);
+        const uint32_t lo1 = __byte_perm(v[2][w], v[3][w], 0x5410);
+        const uint32_t hi0 = __byte_perm(v[0][w], v[1][w], 0x7632);
+        const uint32_t hi1 = __byte_perm(v[2][w], v[3][w], 0x7632);
+        const uint32_t a[4][4] = {
+            {centred<Elt::BF16, 0>(lo0), centred<Elt::BF16, 1>(lo0), centred<Elt::BF16, 0>(lo1), centred<Elt::BF16, 1>(lo1)},
+            {centred<Elt::BF16, 2>(lo0), centred<Elt::BF16, 3>(lo0), centred<Elt::BF16, 2>(lo1), centred<Elt::BF16, 3>(lo1)},
+            {centred<Elt::BF16, 0>(hi0), centred<Elt::BF16, 1>(hi0), centred<Elt::BF16, 0>(hi1), centred<Elt::BF16, 1>(hi1)},
+            {centred<Elt::BF16, 2>(hi0), centred<Elt::BF16, 3>(hi0), centred<Elt::BF16, 2>(hi1), centred<Elt::BF16, 3>(hi1)}};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16n8k16<Elt::BF16>(o[nt][4 * w + i], a[i], pb[nt][0], pb[nt][1]);
+            mma_16n8k16<Elt::BF16>(o[nt][4 * w + i], a[i], pb[nt][2], pb[nt][3]);
+          }
+      }
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -681,7 +723,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
       const int r = nt * 8 + 2 * t + e;
       if (g == 0) {
-        sm_m[warp][r] = m[nt][e];
+        sm_m[warp][r] = bound[nt][e] == -INFINITY ? -INFINITY : m[nt][e];
         sm_l[warp][r] = l[nt][e];
       }
 #pragma unroll
@@ -725,14 +767,17 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// A row's pieces joined by a CTA of four warps: each thread four channels of every
-// (512 / D)-th piece, the sums joined over shared memory.
+// A row's pieces joined by a CTA of kJoinThreads: each thread four channels of every
+// (4 kJoinThreads / D)-th piece, the sums joined over shared memory. 512 threads: the reads of
+// a hundred pieces are then a few loads deep (B1 H32 L131071: @J@).
+constexpr int kJoinThreads = 512;
+
 template <int D, Elt E>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinThreads)
     combine_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
                    uint16_t* __restrict__ O, float* __restrict__ LSE, int n_pieces) {
-  constexpr int T = D / 4, S = 128 / T;  // threads of a piece, pieces at a time
-  __shared__ float sm_top[4], sm_sum[S];
+  constexpr int T = D / 4, S = kJoinThreads / T;  // threads of a piece, pieces at a time
+  __shared__ float sm_top[kJoinThreads / 32], sm_sum[S];
   __shared__ float4 sm_o[S][T];
   pdl_wait();
   pdl_launch_dependents();
@@ -741,12 +786,13 @@ __global__ void __launch_bounds__(128)
   const int at = threadIdx.x % T, first = threadIdx.x / T;
   const float2* ml = part_ml + row * n_pieces;
   float top = -INFINITY;
-  for (int k = threadIdx.x; k < n_pieces; k += 128) top = fmaxf(top, ml[k].x);
+  for (int k = threadIdx.x; k < n_pieces; k += kJoinThreads) top = fmaxf(top, ml[k].x);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) sm_top[warp] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(sm_top[0], sm_top[1]), fmaxf(sm_top[2], sm_top[3]));
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, sm_top[w]);
   const float base = top == -INFINITY ? 0.0f : top;
   const float4* src = reinterpret_cast<const float4*>(part_o) + row * n_pieces * T + at;
   float sum = 0.0f;
@@ -767,7 +813,7 @@ __global__ void __launch_bounds__(128)
   if (at == 0) sm_sum[first] = sum;
   __syncthreads();
   if (first != 0) return;
-#pragma unroll
+#pragma unroll 4
   for (int k = 1; k < S; ++k) {
     const float4 v = sm_o[k][at];
     sum += sm_sum[k];

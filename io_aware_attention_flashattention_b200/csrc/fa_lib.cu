@@ -1169,30 +1169,38 @@ fa_status cache4_rows_impl(const void* K, const void* V, void* codes, void* para
   }
 }
 
-// How an attend call is cut: query rows per CTA (8 or 16), pieces of a sequence and groups of
-// 16 tokens per piece, from the bound on the lengths that the caller gives.
+// How an attend call is cut: query rows per CTA (8 or 16), pieces of a sequence and steps of
+// 32 tokens per piece, from the bound on the lengths that the caller gives.
 struct AttendPlan {
   int rows, nt, row_tiles, piece, n_pieces;
 };
 
-constexpr long long kAttendCtas = 148 * 3;  // one wave (registers allow three CTAs per SM)
-constexpr int kMinPiece = 2 * cache4::kWarps;  // groups: two per warp
+constexpr long long kAttendCtas = 148 * 3;
+constexpr long long kAttendFine = 6;
+constexpr int kMinPiece = cache4::kWarps;   // steps: one per warp
 
+// Few heads are cut into many pieces of equal work, one wave of CTAs; more pieces cost more
+// to join and leave each warp fewer steps behind its start (kAttendCtas 296 / 444 / 592 / 1184:
+// B8 H16 Hkv4 five tokens over 2047 keys 20.9 / 17.9 / 20.4 / 21.2 us, B1 H32 Hkv4 L131071 37.8
+// us up to 592 and 45 us at 1184). Where there are many heads their sequences differ in length,
+// and finer pieces even that out (B64 H32 Hkv8, lengths 2048 to 8192: kAttendFine 1 / 2 / 4 / 6
+// / 8: 216 / 151 / 134 / 130 / 131 us).
 AttendPlan attend_plan(int B, int H, int Hkv, int Nq, int max_len, int window_left) {
   AttendPlan a;
   a.rows = H / Hkv * Nq;
   a.nt = a.rows <= 8 ? 1 : 2;
   a.row_tiles = (a.rows + 8 * a.nt - 1) / (8 * a.nt);
   long long span = std::max(max_len, 1);
-  if (window_left >= 0) span = std::min<long long>(span, static_cast<long long>(window_left) + Nq + 15);
-  const long long groups = (span + cache4::kGroup - 1) / cache4::kGroup;
+  if (window_left >= 0)
+    span = std::min<long long>(span, static_cast<long long>(window_left) + Nq + cache4::kStep - 1);
+  const long long steps = (span + cache4::kStep - 1) / cache4::kStep;
   const long long heads = static_cast<long long>(B) * Hkv * a.row_tiles;
-  const long long ctas = heads * 4 <= kAttendCtas ? kAttendCtas : 4 * kAttendCtas;
+  const long long ctas = heads * 4 <= kAttendCtas ? kAttendCtas : kAttendFine * kAttendCtas;
   const long long want = (ctas + heads - 1) / heads;
-  long long piece = std::max<long long>((groups + want - 1) / want, kMinPiece);
+  long long piece = std::max<long long>((steps + want - 1) / want, kMinPiece);
   piece = (piece + cache4::kWarps - 1) / cache4::kWarps * cache4::kWarps;
   a.piece = static_cast<int>(piece);
-  a.n_pieces = static_cast<int>((groups + piece - 1) / piece);
+  a.n_pieces = static_cast<int>((steps + piece - 1) / piece);
   return a;
 }
 
@@ -1205,9 +1213,9 @@ size_t attend_ws_bytes(const AttendPlan& a, int B, int H, int Nq, int d) {
 fa_status check_attend(int B, int H, int Hkv, int Nq, int d, int max_len) {
   if (B < 1 || H < 1 || Hkv < 1 || Nq < 0 || max_len < 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  // row indices and grids stay below 2^31, with up to 4 kAttendCtas pieces a row
+  // row indices and grids stay below 2^31, with up to kAttendFine * kAttendCtas pieces a row
   if (static_cast<long long>(B) * H >= (1ll << 31) || Nq > (1 << 24) ||
-      static_cast<long long>(B) * H * std::max(Nq, 1) >= (1ll << 31) / (4 * kAttendCtas))
+      static_cast<long long>(B) * H * std::max(Nq, 1) >= (1ll << 31) / (kAttendFine * kAttendCtas))
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
@@ -1259,6 +1267,7 @@ fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* cod
   p.H = H;
   p.Nq = Nq;
   p.rows = a.rows;
+  p.nq = make_divisor(Nq);
   p.row_tiles = a.row_tiles;
   p.n_pieces = a.n_pieces;
   p.piece = a.piece;
@@ -1275,9 +1284,9 @@ fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* cod
   if (st != FA_OK || a.n_pieces == 1) return st;
   const unsigned blocks = static_cast<unsigned>(rows);
   if (d == 64)
-    return launch(cache4::combine_kernel<64, E>, blocks, 128, 0, s, p.part_o, p.part_ml, p.O, LSE,
+    return launch(cache4::combine_kernel<64, E>, blocks, cache4::kJoinThreads, 0, s, p.part_o, p.part_ml, p.O, LSE,
                   a.n_pieces);
-  return launch(cache4::combine_kernel<128, E>, blocks, 128, 0, s, p.part_o, p.part_ml, p.O, LSE,
+  return launch(cache4::combine_kernel<128, E>, blocks, cache4::kJoinThreads, 0, s, p.part_o, p.part_ml, p.O, LSE,
                 a.n_pieces);
 }
 
