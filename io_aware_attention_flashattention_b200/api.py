@@ -37,6 +37,10 @@ __all__ = [
 ]
 
 
+_Tensor, _Stream = torch.Tensor, torch.cuda.Stream
+_current_device = torch.cuda.current_device
+
+
 def _one_device(*args):
     """A context that makes current the one CUDA device of a call's tensors (and
     stream): the library launches on the current device, and a stream left as None
@@ -57,10 +61,10 @@ def _on_one_device(fn):
     def call(*args, **kwargs):
         # The common case, everything on the current GPU, without a context to enter.
         index = -1
-        for a in (*args, *kwargs.values()):
-            if isinstance(a, torch.Tensor):
+        for a in (*args, *kwargs.values()) if kwargs else args:
+            if isinstance(a, _Tensor):
                 i = a.get_device()  # -1 on the CPU
-            elif isinstance(a, torch.cuda.Stream):
+            elif isinstance(a, _Stream):
                 i = a.device.index
             else:
                 continue
@@ -69,7 +73,7 @@ def _on_one_device(fn):
                     break
                 index = i
         else:
-            if index < 0 or index == torch.cuda.current_device():
+            if index < 0 or index == _current_device():
                 return fn(*args, **kwargs)
         with _one_device(*args, *kwargs.values()):
             return fn(*args, **kwargs)
@@ -78,7 +82,7 @@ def _on_one_device(fn):
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     return int(getattr(stream, "cuda_stream", stream))
 
 
@@ -89,7 +93,7 @@ def _shape(t: torch.Tensor):
 
 
 def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape) -> int:
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape
+    if (isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
             and t.is_contiguous()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
@@ -109,8 +113,16 @@ def fa_version() -> str:
     return lib().fa_version().decode()
 
 
+@functools.lru_cache(maxsize=1024)  # a function of its arguments alone
 def fa_backward_workspace_size(B: int, H: int, N: int, d: int) -> int:
     return int(lib().fa_backward_workspace_size(B, H, N, d))
+
+
+@functools.lru_cache(maxsize=1024)
+def fa_cache4_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int, max_len: int,
+                             window_left: int = -1) -> int:
+    """Bytes of workspace that fa_cache4_attend needs."""
+    return int(lib().fa_cache4_workspace_size(B, H, Hkv, Nq, d, max_len, window_left))
 
 
 @_on_one_device
@@ -456,12 +468,12 @@ def fa_backward_scored_f16(Q, K, V, O, dO, LSE, dQ, dK, dV, scale: float, causal
 
 def _cache4(codes, params, page_table, dtype, B, Hkv, d):
     """(codes, params, page table pointers), (page, n_pages, max_pages)."""
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 5:
+    if not isinstance(codes, _Tensor) or codes.dim() != 5:
         raise ValueError("codes must be a [pages, 2, K/V heads, page, d / 2] tensor")
-    n_pages, _, _, page, _ = (int(x) for x in codes.shape)
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+    n_pages, _, _, page, _ = codes.shape
+    if not isinstance(page_table, _Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a [B, pages per sequence] tensor")
-    max_pages = int(page_table.shape[1])
+    max_pages = page_table.shape[1]
     return ((_need("codes", codes, torch.uint8, (n_pages, 2, Hkv, page, d // 2)),
              _need("params", params, dtype, (n_pages, 2, Hkv, page, 2)),
              _need("page_table", page_table, torch.int32, (B, max_pages))),
@@ -596,7 +608,7 @@ def forward(q, k, v, causal: bool = False, scale=None, window=None, block_mask=N
     B, H, N, d = _shape(q)
     scale = _default_scale(d, scale)
     o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    lse = q.new_empty((B, H, N), dtype=torch.float32)
     if _scored(q, k, window, block_mask, dropout, softcap, slopes, documents, prefix):
         fn = fa_forward_scored_f16 if _check_scored(q, block_mask, dropout) else fa_forward_scored
         fn(q, k, v, o, lse, scale, causal, window, softcap, slopes, documents, prefix)
@@ -717,24 +729,26 @@ def cache4_empty(n_pages: int, kv_heads: int, page: int, d: int, dtype=torch.bfl
             torch.empty(n_pages, 2, kv_heads, page, 2, dtype=dtype, device=device))
 
 
+@_on_one_device
 def cache4_append(codes, params, k, v, page_table, positions, counts=None) -> None:
     """Puts k, v ([B, kv heads, n, d], bf16 or f16) into the cache: token t of sequence b at
     position positions[b] + t, for t < counts[b] (all n without counts)."""
-    fn = fa_cache4_append_f16 if _cache4_suffix(k.dtype) else fa_cache4_append
-    fn(k, v, codes, params, page_table, positions, counts)
+    _cache4_rows("fa_cache4_append" + _cache4_suffix(k.dtype), k.dtype, k, v, codes, params,
+                 page_table, positions, counts, None)
 
 
+@_on_one_device
 def cache4_read(codes, params, page_table, positions, n: int, counts=None):
     """(k, v), [B, kv heads, n, d], as the cache holds them at positions[b] .. positions[b] +
     n - 1; zeros behind counts[b]."""
     shape = (page_table.shape[0], codes.shape[2], n, 2 * codes.shape[4])
-    k = torch.empty(shape, dtype=params.dtype, device=codes.device)
-    v = torch.empty_like(k)
-    fn = fa_cache4_read_f16 if _cache4_suffix(params.dtype) else fa_cache4_read
-    fn(k, v, codes, params, page_table, positions, counts)
+    k, v = params.new_empty(shape), params.new_empty(shape)
+    _cache4_rows("fa_cache4_read" + _cache4_suffix(params.dtype), params.dtype, k, v, codes,
+                 params, page_table, positions, counts, None)
     return k, v
 
 
+@_on_one_device
 def cache4_attend(q, codes, params, page_table, lengths, scale=None, window_left: int = -1,
                   softcap=None, slopes=None, max_len=None):
     """(O, LSE) of the last tokens q ([B, H, n, d]; n = 1 when decoding) of sequences of
@@ -742,13 +756,13 @@ def cache4_attend(q, codes, params, page_table, lengths, scale=None, window_left
     ``forward``, causal. ``max_len``: a bound on the lengths known on the host (default: what
     the page table has room for); a close one gives a better cut of the work."""
     B, H, n, d = _shape(q)
-    room = int(page_table.shape[1]) * int(codes.shape[3])
+    room = page_table.shape[1] * codes.shape[3]
     max_len = room if max_len is None else min(int(max_len), room)
     o = torch.empty_like(q)
-    lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
-    nbytes = lib().fa_cache4_workspace_size(B, H, int(codes.shape[2]), n, d, max_len, window_left)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    fn = fa_cache4_attend_f16 if _cache4_suffix(q.dtype) else fa_cache4_attend
-    fn(q, o, lse, codes, params, page_table, lengths, max_len, _default_scale(d, scale),
-       window_left, softcap, slopes, ws)
+    lse = q.new_empty((B, H, n), dtype=torch.float32)
+    nbytes = fa_cache4_workspace_size(B, H, codes.shape[2], n, d, max_len, window_left)
+    ws = q.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    _cache4_attend("fa_cache4_attend" + _cache4_suffix(q.dtype), q.dtype, q, o, lse, codes, params,
+                   page_table, lengths, max_len, _default_scale(d, scale), window_left, softcap,
+                   slopes, ws, None)
     return o, lse
