@@ -288,9 +288,13 @@ fa_status fa_backward_dropout_heads(const void* Q, const void* K, const void* V,
  *     and window_right say (window_left holds for them too). Negative counts as 0.
  *   causal, window_left, window_right: as for fa_forward_masked.
  * The tensors must be finite at padding positions as well (weights of 0 multiply them).
- * n_docs is not read without documents. Workspace: fa_backward_workspace_size(B, H, N, d).
- * Other arguments, errors and determinism as for fa_forward / fa_backward.
+ * n_docs is not read without documents. Workspace: fa_backward_scored_workspace_size bytes;
+ * fa_backward_workspace_size(B, H, N, d) is enough to run, but where key tiles are few it may
+ * leave no room to part the query heads of a K/V head over several CTAs (dK and dV then
+ * differ in the last bits). Other arguments, errors and determinism as for fa_forward /
+ * fa_backward.
  */
+size_t fa_backward_scored_workspace_size(int B, int H, int Hkv, int N, int d);
 fa_status fa_forward_scored(const void* Q, const void* K, const void* V, void* O, float* LSE,
                             int B, int H, int Hkv, int N, int d, float scale, int causal,
                             int window_left, int window_right, float softcap,

@@ -70,6 +70,7 @@ SIGNATURES = {
     "fa_cache4_attend_f16": _CACHE4_ATTEND,
     "fa_cache4_workspace_size": (_sz, [_i] * 7),
     "fa_cache4_row": (_i64, [_vp, _i, _i64, _i, _i, _i, _i, _i64]),
+    "fa_backward_scored_workspace_size": (_sz, [_i] * 5),
     "fa_score_span": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp]),
     "fa_get_status": (_i, [_vp]),
     "fa_watchdog_selftest": (_i, [_i, _vp]),

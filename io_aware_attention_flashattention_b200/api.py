@@ -119,6 +119,12 @@ def fa_backward_workspace_size(B: int, H: int, N: int, d: int) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
+def fa_backward_scored_workspace_size(B: int, H: int, Hkv: int, N: int, d: int) -> int:
+    """Bytes of workspace that fa_backward_scored makes use of."""
+    return int(lib().fa_backward_scored_workspace_size(B, H, Hkv, N, d))
+
+
+@functools.lru_cache(maxsize=1024)
 def fa_cache4_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int, max_len: int,
                              window_left: int = -1) -> int:
     """Bytes of workspace that fa_cache4_attend needs."""
@@ -644,8 +650,15 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale=None, workspace=No
     B, H, N, d = _shape(q)
     scale = _default_scale(d, scale)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws = workspace_for(q) if workspace is None else workspace
-    if _scored(q, k, window, block_mask, dropout, softcap, slopes, documents, prefix):
+    scored = _scored(q, k, window, block_mask, dropout, softcap, slopes, documents, prefix)
+    if workspace is not None:
+        ws = workspace
+    elif scored:
+        ws = q.new_empty(max(1, fa_backward_scored_workspace_size(B, H, _shared_heads(q, k)[2], N, d)),
+                         dtype=torch.uint8)
+    else:
+        ws = workspace_for(q)
+    if scored:
         fn = (fa_backward_scored_f16 if _check_scored(q, block_mask, dropout)
               else fa_backward_scored)
         fn(q, k, v, o, do, lse, dq, dk, dv, scale, causal, ws, window, softcap, slopes,

@@ -127,7 +127,10 @@ struct Params {
   // the second to arrive adds the two slots (segment 0 first) and writes dK, dV.
   int n_split;
   int split_num;
-  float* part;         // [n_split][2 segments][dK, dV][128 key rows][D] fp32
+  // kScore: every key tile is run by n_seg CTAs, each for an equal part of the query heads that
+  // share the K/V head; their fp32 partials are joined as those of a split tile, in order.
+  int n_seg;
+  float* part;         // [n_split][2 segments][dK, dV][128 key rows][D] fp32 (kScore: [tiles][n_seg])
   unsigned* arrivals;  // [n_split] (zeroed by the preprocess)
   // Grid order of the key tiles: head-major (0: the CTAs resident at one time share one
   // or two heads' Q, dO and dQ accumulator in L2) or rank-major (1: every head's key tile
@@ -275,6 +278,8 @@ __global__ void __launch_bounds__(256)
 constexpr int kFewKeys = 16;
 
 struct PreParams {
+  unsigned* arrivals;  // of the main kernel's segments, zeroed here
+  int n_arrivals;
   const uint16_t* O;
   const uint16_t* dO;
   const uint16_t* Q;
@@ -298,6 +303,8 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_scored_kernel(const PreParams 
   pdl_wait();  // the grid before this one (the forward) has completed
   pdl_launch_dependents();
   constexpr int kRows = 8, G = D / 8, S = 32 / G;  // lanes of a row, rows at a time
+  if (blockIdx.x == 0)
+    for (int k = threadIdx.x; k < p.n_arrivals; k += blockDim.x) p.arrivals[k] = 0u;
   const int lane = threadIdx.x & 31;
   const long long r = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kRows;
   const int bh = static_cast<int>(r / p.Npad);  // Npad is a multiple of 128: one head's rows
@@ -605,7 +612,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_whole = n_tiles - p.n_split;
   // this CTA's key tile and, for a split tile, which segment (-1: the whole tile)
   int tile = static_cast<int>(blockIdx.x), seg = -1;
-  if (tile >= n_whole) {
+  if (kScore != 0 && p.n_seg > 1) {
+    seg = tile % p.n_seg;
+    tile /= p.n_seg;
+  }
+  if (kScore == 0 && tile >= n_whole) {
     const int c = tile - n_whole;                  // [larger segments][smaller segments]
     const bool second_half = c >= p.n_split;
     tile = n_whole + (second_half ? c - p.n_split : c);
@@ -622,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int i_hi_tile = (wl < 0) ? n_q : min(n_q, (k1 + wl) / BM + 1);
   // kScore: bh is a K/V head; the CTA walks the query tiles of each head that shares it,
   // one head after the other. docs, prefix: this batch entry's own.
-  const int n_share = kScore ? p.score.group : 1;
+  const int n_share = kScore ? p.score.group / p.n_seg : 1;
   const int b_of = kScore ? bh / (p.score.H / p.score.group) : 0;
   const int* const docs =
       (kScore && p.score.docs) ? p.score.docs + static_cast<size_t>(b_of) * (p.score.n_docs + 1)
@@ -638,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // a split tile's segment walks a sub-range of the query tiles (no block mask then)
   int i_lo = i_lo_tile, i_hi = i_hi_tile;
-  if (seg >= 0) {
+  if (kScore == 0 && seg >= 0) {
     const int a = split_point(i_hi_tile - i_lo_tile, p.split_num);
     if (seg == 0) i_hi = i_lo_tile + a; else i_lo = i_lo_tile + a;
   }
@@ -709,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       do ++i; while (!member(i));
     }
   };
-  const int bhq0 = kScore ? bh * n_share : bh;
+  const int bhq0 = kScore ? bh * p.score.group + max(seg, 0) * n_share : bh;
 
   // ring of half tiles: seq = 4*step + 2*h + w, w = 0 for dO (rows 64h.. of query
   // tile i), w = 1 for Q (with L2 and D of those 64 queries)
@@ -933,10 +944,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tm_acc = tmem + lane_off + (h == 0 ? C::kTmDK : C::kTmDV);
       uint16_t* out = (h == 0 ? p.dK : p.dV) + (static_cast<size_t>(bh) * p.N + key) * D;
       const float mul = (h == 0) ? p.scale : 1.0f;
-      const int ksplit = tile - n_whole;
+      const int ksplit = kScore ? tile : tile - n_whole;
+      const int n_seg = kScore ? p.n_seg : 2;
       // slot layout: [split tile][segment][dK, dV][128 key rows][D]
       auto slot_row = [&](int sg) -> float* {
-        return p.part + ((static_cast<size_t>(ksplit) * 2 + sg) * 2 + h) * (BN * D) +
+        return p.part + ((static_cast<size_t>(ksplit) * n_seg + sg) * 2 + h) * (BN * D) +
                static_cast<size_t>(krow) * D;
       };
 #pragma unroll 1
@@ -978,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kBarSplitDecided), 0, wd));
-        if (ok && *arrived == 1u) {
+        if (ok && *arrived == static_cast<unsigned>(n_seg - 1)) {
           __threadfence();
           const float4* s0 = reinterpret_cast<const float4*>(slot_row(0));
           const float4* s1 = reinterpret_cast<const float4*>(slot_row(1));
@@ -989,6 +1001,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < 8; ++u) {
               a[u] = __ldcg(s0 + cc * 8 + u);
               b[u] = __ldcg(s1 + cc * 8 + u);
+            }
+            if constexpr (kScore != 0) {
+              for (int sg = 2; sg < n_seg; ++sg) {  // ((0 + 1) + 2) + ...: b takes the last one
+                const float4* s2 = reinterpret_cast<const float4*>(slot_row(sg));
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                  a[u] = make_float4(a[u].x + b[u].x, a[u].y + b[u].y, a[u].z + b[u].z,
+                                     a[u].w + b[u].w);
+                  b[u] = __ldcg(s2 + cc * 8 + u);
+                }
+              }
             }
             uint32_t pk[16];
 #pragma unroll

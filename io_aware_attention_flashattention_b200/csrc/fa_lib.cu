@@ -1016,6 +1016,29 @@ fa_status launch_bwd_scored(int d, unsigned grid, cudaStream_t s, const CUtensor
                 bwd::Cfg<128>::kSmemBytes, s, mq, mk, mv, mdo, p);
 }
 
+// Segments of the scored backward: CTAs per key tile, each for an equal part of the query heads
+// of its K/V head. Sharing leaves fewer key tiles than SMs on short rows (B3 Hkv2 N1531: 72 of
+// 148); then the group is parted until two waves of CTAs are reached. Each segment writes 256 D
+// fp32 partials and the last one reads them all back, which more CTAs than that do not repay.
+int score_segments(long long BHkv, int group, int N) {
+  const long long tiles = BHkv * ((static_cast<long long>(N) + 127) / 128);
+  int seg = 1;
+  if (tiles >= 148) return seg;
+  for (int s = 2; s <= group; ++s)
+    if (group % s == 0 && tiles * seg < 2 * 148) seg = s;
+  return seg;
+}
+
+// Workspace with room for the segments: the base regions, partials, arrival counters.
+size_t scored_ws_bytes(long long BH, long long BHkv, int N, int d) {
+  const int seg = score_segments(BHkv, static_cast<int>(BH / BHkv), N);
+  const size_t base = backward_ws_bytes(BH, N, d, 0);
+  if (seg == 1) return base;
+  const size_t tiles = static_cast<size_t>(BHkv) * ((static_cast<size_t>(N) + 127) / 128);
+  return base + round256(tiles * seg * 2 * 128 * d * sizeof(float)) +
+         round256(tiles * sizeof(unsigned));
+}
+
 template <Elt E>
 fa_status backward_scored_impl(const void* Q, const void* K, const void* V, const void* O,
                                const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
@@ -1034,9 +1057,21 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
   if ((st = make_score(B, H, Hkv, scale, softcap, slopes, documents, n_docs, prefix, &p.score)) !=
       FA_OK)
     return st;
-  st = bwd_plan(ptrs, 9, B, H, N, d, scale, causal, workspace, workspace_bytes, &pl);
+  // a workspace without room for segments runs whole key tiles
+  st = bwd_plan(ptrs, 9, B, H, N, d, scale, causal, workspace, workspace_bytes, &pl, false);
   if (st != FA_OK || N == 0) return st;
+  const int BHkv = B * Hkv;
+  const long long n_tiles = static_cast<long long>(BHkv) * (pl.Npad / bwd::BN);
+  p.n_seg = workspace_bytes >= scored_ws_bytes(pl.BH, BHkv, N, d)
+                ? score_segments(BHkv, p.score.group, N)
+                : 1;
+  p.part = pl.part;
+  p.arrivals = reinterpret_cast<unsigned*>(
+      reinterpret_cast<char*>(pl.part) +
+      round256(static_cast<size_t>(n_tiles) * p.n_seg * 2 * 128 * d * sizeof(float)));
   bwd::PreParams pre;
+  pre.arrivals = p.arrivals;
+  pre.n_arrivals = p.n_seg > 1 ? static_cast<int>(n_tiles) : 0;
   pre.O = static_cast<const uint16_t*>(O);
   pre.dO = static_cast<const uint16_t*>(dO);
   pre.Q = static_cast<const uint16_t*>(Q);
@@ -1059,7 +1094,6 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
                : launch(bwd::fa_bwd_pre_scored_kernel<128, E>, pre_blocks, 256, 0, s, pre);
   if (st != FA_OK) return st;
   CUtensorMap mq, mk, mv, mdo;
-  const int BHkv = B * Hkv;
   if (!make_map<E>(&mq, Q, pl.BH, N, d, 64) || !make_map<E>(&mk, K, BHkv, N, d, bwd::BN) ||
       !make_map<E>(&mv, V, BHkv, N, d, bwd::BN) || !make_map<E>(&mdo, dO, pl.BH, N, d, 64))
     return FA_ERR_CUDA;
@@ -1080,15 +1114,12 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
   p.timeout_ns = watchdog_ns();
   p.n_split = 0;
   p.split_num = 8;
-  p.part = pl.part;
-  p.arrivals = pl.arrivals;
   // the plain backward's rule for the order of the key tiles
-  const long long n_tiles = static_cast<long long>(BHkv) * (pl.Npad / bwd::BN);
   p.rank_major = (mask.wr >= 0 || mask.wl >= 0) && n_tiles > device_sms() &&
                          static_cast<double>(pl.BH) * N * d * 8.0 <= kBwdRankMajorBytes
                      ? 1
                      : 0;
-  const unsigned grid = static_cast<unsigned>(n_tiles);
+  const unsigned grid = static_cast<unsigned>(n_tiles * p.n_seg);
   constexpr int On = kScoreOn, Cap = kScoreCap, Bias = kScoreBias;
   switch (score_bits(softcap, slopes)) {
     case On: st = launch_bwd_scored<E, On>(d, grid, s, mq, mk, mv, mdo, p); break;
@@ -1097,7 +1128,7 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
     default: st = launch_bwd_scored<E, On | Cap | Bias>(d, grid, s, mq, mk, mv, mdo, p);
   }
   if (st != FA_OK) return st;
-  return dq_convert_impl<E>(dQ, B, H, N, d, scale, workspace, workspace_bytes, stream);
+  return dq_convert_impl<E>(dQ, B, H, N, d, scale, workspace, workspace_bytes, stream, false);
 }
 
 // ---------------------------------------------------------------- 4-bit cache
@@ -1355,6 +1386,11 @@ fa_status fa_score_span(const int32_t* documents, int n_docs, const int32_t* pre
   *lo = s.lo;
   *hi = s.hi;
   return FA_OK;
+}
+
+size_t fa_backward_scored_workspace_size(int B, int H, int Hkv, int N, int d) {
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || N < 1 || (d != 64 && d != 128)) return 0;
+  return scored_ws_bytes(static_cast<long long>(B) * H, static_cast<long long>(B) * Hkv, N, d);
 }
 
 float fa_dropout_rate(float p_drop) {

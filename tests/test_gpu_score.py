@@ -103,6 +103,27 @@ def test_forward_and_backward(case):
     check(got, q, k, v, do, mask, scale, rest.get("softcap"), kw.get("slopes"))
 
 
+@pytest.mark.parametrize("H,Hkv", [(6, 1), (8, 2), (4, 4)])
+def test_segments_of_a_group(H, Hkv):
+    """Key tiles run by several CTAs, a part of the group's heads each: the same from run to
+    run, within the bounds, and as whole tiles in the last bits; whatever the workspace held."""
+    B, N, d = 2, 300, 64
+    q, k, v, do = make(B, H, Hkv, N, d, BF, seed=H)
+    docs = torch.tensor([[0, 150, 290], [0, 0, 300]], dtype=torch.int32, device="cuda")
+    kw = dict(softcap=10.0, documents=docs)
+    o, lse = api.forward(q, k, v, causal=True, **kw)
+    outs = []
+    for fill in (0xFF, 0x01):
+        ws = torch.full((api.fa_backward_scored_workspace_size(B, H, Hkv, N, d),), fill, dtype=torch.uint8,
+                        device="cuda")
+        outs.append(api.backward(q, k, v, o, lse, do, causal=True, workspace=ws, **kw))
+    assert torch.equal(outs[0][1], outs[1][1]) and torch.equal(outs[0][2], outs[1][2])
+    mask = ref.visible(B, N, True, documents=docs.tolist())
+    check((o, lse) + outs[0], q, k, v, do, mask, 0.125, 10.0, None)
+    whole = api.backward(q, k, v, o, lse, do, causal=True, workspace=api.workspace_for(q), **kw)
+    check((o, lse) + whole, q, k, v, do, mask, 0.125, 10.0, None)
+
+
 @pytest.mark.parametrize("cap,gain", [(0.01, 1.0), (1.0, 4.0), (5.0, 30.0), (50.0, 60.0), (1e4, 1.0), (1e6, 8.0)])
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_caps_far_from_the_scores_size(cap, gain, dtype):

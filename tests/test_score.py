@@ -158,6 +158,17 @@ def test_scored_calls_refuse_on_the_host(libfa, suffix):
     assert bwd(dq=None) == 1
 
 
+def test_scored_workspace_size(libfa):
+    f, base = libfa.fa_backward_scored_workspace_size, libfa.fa_backward_workspace_size
+    assert f(3, 8, 3, 1531, 64) == 0 and f(3, 8, 2, 1531, 96) == 0 and f(1, 8, 2, 0, 64) == 0
+    # 72 key tiles of 4 heads each: two waves of 148 take 4 segments each, dK and dV partials
+    # of 128 rows in fp32, and a counter per tile
+    assert f(3, 8, 2, 1531, 64) == base(3, 8, 1531, 64) + 72 * 4 * 2 * 128 * 64 * 4 + 512
+    assert f(2, 16, 4, 4096, 128) == base(2, 16, 4096, 128)  # 256 tiles: whole
+    assert f(1, 6, 1, 128, 64) == base(1, 6, 128, 64) + 6 * 2 * 128 * 64 * 4 + 256
+    assert f(1, 8, 8, 128, 64) == base(1, 8, 128, 64)  # nothing to part
+
+
 def test_binding_refuses_what_does_not_combine():
     from io_aware_attention_flashattention_b200 import api
 
