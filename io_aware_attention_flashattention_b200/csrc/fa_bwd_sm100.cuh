@@ -57,6 +57,7 @@ namespace bwd {
 constexpr int BM = 128;        // query rows per step
 constexpr int BN = 128;        // key rows per CTA
 constexpr int kThreads = 512;
+constexpr int kThreadsScore = 704;  // kScore instances: 16 P/dS warps instead of 8
 constexpr int kWarpDq = 8;     // first of the 4 dQ warps
 constexpr int kWarpTma = 12;
 constexpr int kWarpMma = 13;
@@ -183,13 +184,14 @@ __device__ __forceinline__ void issue_xyT_half(uint32_t tm_d, uint32_t x_smem, u
 
 // acc[128 keys x D] (+)= A_tmem[128 keys x 64 queries] * Y_h[64 queries x D] (the half
 // tile, row-major in shared memory, used as the MN-major B operand).
-template <int D, Elt E>
+// kQuarters: A's columns lie in two pieces of 16, 32 apart (p_ds_quarter).
+template <int D, Elt E, bool kQuarters = false>
 __device__ __forceinline__ void issue_acc_half(uint32_t tm_acc, uint32_t tm_a, uint32_t yh_smem,
                                                bool accumulate) {
   constexpr uint32_t idesc = idesc_f32acc<E>(128, D, 0, 1);
 #pragma unroll
   for (int kk = 0; kk < 64 / 16; ++kk)
-    mma_ts_e(tm_acc, tm_a + kk * 8,
+    mma_ts_e(tm_acc, tm_a + (kQuarters ? (kk / 2) * 32 + (kk % 2) * 8 : kk * 8),
              sdesc_sw128(yh_smem + kk * 2048, Cfg<D>::kHalfChunkBytes, 1024), idesc,
              (accumulate || kk > 0) ? 1u : 0u);
 }
@@ -335,6 +337,8 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_scored_kernel(const PreParams 
       p.score.docs ? p.score.docs + static_cast<size_t>(b) * (p.score.n_docs + 1) : nullptr;
   const int* prefix =
       p.score.prefix ? p.score.prefix + static_cast<size_t>(b) * p.score.n_docs : nullptr;
+  __shared__ int shared_docs[256];
+  share_documents(shared_docs, 256, p.score.n_docs, docs, prefix);
   if (lane < n) {
     const float lse = p.LSE[row0 + lane];
     if (lse != -INFINITY) l2 = lse * 1.4426950408889634f;
@@ -443,26 +447,12 @@ __global__ void __launch_bounds__(256)
 // kM: test each query against the key's visible range [q_lo, q_hi): query qh0 + x is
 // visible iff qoff + x < q_span (unsigned). ctr_head: the dropout counter's head word
 // (the call's head_base + the flattened head).
-// kScore: S^T is first brought to the shaped score (c turns it to log2 units); with a cap
-// dS takes the factor 1 - tanh^2, the derivative of the capped score by scale * q.k. lone:
-// the query (counted from qh0) that sees this key alone, if any: its dS = P (dP - D) is 0
-// exactly, where dP and D, summed in different orders, would leave their rounding. Such a
-// query has the key's own index, and steps that hold one always test elements (kM).
-template <Elt E, bool kDropout, bool kM, int kScore = 0>
+template <Elt E, bool kDropout, bool kM>
 __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const float4* Lv,
                                           const float4* Dv4, float c, int key, int qh0,
                                           uint32_t ctr_head,
                                           const DropoutParams& drop, int lane, int qoff,
-                                          unsigned q_span, uint8_t* ds_row, int krow,
-                                          const ScoreParams& score, float slope_neg,
-                                          int lone) {
-  // kScore: the queries [-qoff, -qoff + q_span) of the half that see this key, as bits
-  [[maybe_unused]] uint32_t seen[2] = {0u, 0u};
-  if constexpr (kScore != 0 && kM) {
-    const int hi = static_cast<int>(q_span) - qoff;
-    seen[0] = span_bits(-qoff, hi);
-    seen[1] = span_bits(-qoff - 32, hi - 32);
-  }
+                                          unsigned q_span, uint8_t* ds_row, int krow) {
   uint32_t sv[2][16], dv[2][16];
   tmem_ld16(tm_s, sv[0]);
   tmem_ld16(tm_dp, dv[0]);
@@ -474,15 +464,6 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
       tmem_ld16(tm_s + 16 * (cc + 1), sv[cur ^ 1]);
       tmem_ld16(tm_dp + 16 * (cc + 1), dv[cur ^ 1]);
     }
-    // tanh of the chunk's scores, kept apart from the bias for the derivative
-    [[maybe_unused]] uint32_t th[(kScore & kScoreCap) ? 16 : 1];
-    if constexpr ((kScore & kScoreCap) != 0) {
-      tanh_scores<16>(sv[cur], score);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) th[k] = sv[cur][k];
-    }
-    if constexpr ((kScore & kScoreBias) != 0)
-      bias_scores(sv[cur], qh0 + 16 * cc - key, slope_neg);
     // Dropout bytes of this key for the chunk's 16 queries: byte e of zq[v] is
     // query 16cc + 4v + e of the half. One block covers 4 queries x 4 keys, and
     // the lanes of keys 4g..4g+3 share its counter: lane u draws the block of the
@@ -506,37 +487,6 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
       transpose4_lanes(zq, u);
     }
     uint32_t pk[8], dk[8];
-    if constexpr (kScore != 0) {
-      // in pairs: P = 2^(S c - L2), dS = P (dP - D) (1 - tanh^2)
-#pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        const int k = 2 * v;
-        const float4 L4 = Lv[cc * 4 + v / 2], D4 = Dv4[cc * 4 + v / 2];
-        const float2 nl = (v & 1) ? make_float2(-L4.z, -L4.w) : make_float2(-L4.x, -L4.y);
-        const float2 nd = (v & 1) ? make_float2(-D4.z, -D4.w) : make_float2(-D4.x, -D4.y);
-        const float2 x = ffma2(make_float2(__uint_as_float(sv[cur][k]),
-                                           __uint_as_float(sv[cur][k + 1])),
-                               make_float2(c, c), nl);
-        float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        if constexpr (kM) {
-          const uint32_t bits = seen[cc / 2] >> ((cc & 1) * 16 + k);
-          if ((bits & 1u) == 0u) pe.x = 0.f;
-          if ((bits & 2u) == 0u) pe.y = 0.f;
-        }
-        float2 ds = fmul2(pe, fadd2(make_float2(__uint_as_float(dv[cur][k]),
-                                                __uint_as_float(dv[cur][k + 1])), nd));
-        if constexpr ((kScore & kScoreCap) != 0) {
-          const float2 y = make_float2(__uint_as_float(th[k]), __uint_as_float(th[k + 1]));
-          ds = fmul2(ds, ffma2(make_float2(-y.x, -y.y), y, make_float2(1.0f, 1.0f)));
-        }
-        if constexpr (kM) {
-          if (cc * 16 + k == lone) ds.x = 0.0f;
-          if (cc * 16 + k + 1 == lone) ds.y = 0.0f;
-        }
-        pk[v] = pack2<E>(pe.x, pe.y);
-        dk[v] = pack2<E>(ds.x, ds.y);
-      }
-    } else {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const float4 L4 = Lv[cc * 4 + v];
@@ -566,7 +516,6 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
       dk[2 * v] = pack2<E>(dsv[0], dsv[1]);
       dk[2 * v + 1] = pack2<E>(dsv[2], dsv[3]);
     }
-    }
     tmem_st8(tm_s + 8 * cc, pk);
     tmem_st8(tm_dp + 8 * cc, dk);
     // dS into the swizzled shared chunk: 16 queries = 16-byte units 2cc, 2cc+1
@@ -578,10 +527,78 @@ __device__ __forceinline__ void p_ds_half(uint32_t tm_s, uint32_t tm_dp, const f
   }
 }
 
+// Shaped scores: P^T and dS^T of a quarter step (32 queries from q0 on) for one key row. The
+// P/dS work of a half is shared by eight warps, two threads a key row: with one thread a row
+// (64 queries) a step's length was the latency of that thread's chain, 4.8 us at D = 64 with a
+// cap and a bias. tm_s, tm_dp: this thread's 32 columns of S^T and dP^T; P and dS go back to the
+// first 16 of them (so that no thread writes where another still reads). unit0: the first of
+// this thread's 16-byte units of the dS row. seen: bits of the queries that see the key (kM).
+//   P = 2^(S c - L2) with S the shaped score (c turns it to log2 units), dS = P (dP - D), with a
+//   cap times 1 - tanh^2, the derivative of the capped score by scale * q.k.
+// lone: the query (counted from q0) that sees this key alone, if any: its dS = P (dP - D) is 0
+// exactly, where dP and D, summed in different orders, would leave their rounding. Such a
+// query has the key's own index, and steps that hold one always test elements (kM).
+template <Elt E, bool kM, int kScore>
+__device__ __forceinline__ void p_ds_quarter(uint32_t tm_s, uint32_t tm_dp, const float4* Lv,
+                                             const float4* Dv4, float c, int key, int q0,
+                                             uint32_t seen, uint8_t* ds_row, int krow, int unit0,
+                                             const ScoreParams& score, float slope_neg,
+                                             int lone) {
+#pragma unroll
+  for (int cc = 0; cc < 2; ++cc) {
+    uint32_t sv[16], dv[16];
+    tmem_ld16(tm_s + 16 * cc, sv);
+    tmem_ld16(tm_dp + 16 * cc, dv);
+    tmem_wait_ld();
+    // tanh of the chunk's scores, kept apart from the bias for the derivative
+    [[maybe_unused]] uint32_t th[(kScore & kScoreCap) ? 16 : 1];
+    if constexpr ((kScore & kScoreCap) != 0) {
+      tanh_scores<16>(sv, score);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) th[k] = sv[k];
+    }
+    if constexpr ((kScore & kScoreBias) != 0) bias_scores(sv, q0 + 16 * cc - key, slope_neg);
+    uint32_t pk[8], dk[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const int k = 2 * v;
+      const float4 L4 = Lv[cc * 4 + v / 2], D4 = Dv4[cc * 4 + v / 2];
+      const float2 nl = (v & 1) ? make_float2(-L4.z, -L4.w) : make_float2(-L4.x, -L4.y);
+      const float2 nd = (v & 1) ? make_float2(-D4.z, -D4.w) : make_float2(-D4.x, -D4.y);
+      const float2 x = ffma2(make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])),
+                             make_float2(c, c), nl);
+      float2 pe = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      if constexpr (kM) {
+        if (((seen >> (16 * cc + k)) & 1u) == 0u) pe.x = 0.f;
+        if (((seen >> (16 * cc + k + 1)) & 1u) == 0u) pe.y = 0.f;
+      }
+      float2 ds = fmul2(
+          pe, fadd2(make_float2(__uint_as_float(dv[k]), __uint_as_float(dv[k + 1])), nd));
+      if constexpr ((kScore & kScoreCap) != 0) {
+        const float2 y = make_float2(__uint_as_float(th[k]), __uint_as_float(th[k + 1]));
+        ds = fmul2(ds, ffma2(make_float2(-y.x, -y.y), y, make_float2(1.0f, 1.0f)));
+      }
+      if constexpr (kM) {
+        if (16 * cc + k == lone) ds.x = 0.0f;
+        if (16 * cc + k + 1 == lone) ds.y = 0.0f;
+      }
+      pk[v] = pack2<E>(pe.x, pe.y);
+      dk[v] = pack2<E>(ds.x, ds.y);
+    }
+    tmem_st8(tm_s + 8 * cc, pk);
+    tmem_st8(tm_dp + 8 * cc, dk);
+    const int u = unit0 + 2 * cc;
+    *reinterpret_cast<uint4*>(ds_row + ((u ^ (krow & 7)) * 16)) =
+        make_uint4(dk[0], dk[1], dk[2], dk[3]);
+    *reinterpret_cast<uint4*>(ds_row + (((u + 1) ^ (krow & 7)) * 16)) =
+        make_uint4(dk[4], dk[5], dk[6], dk[7]);
+  }
+}
+
 // ------------------------------------------------------------------ main kernel
 
 template <int D, Elt E, bool kMasked, bool kDropout = false, int kScore = 0>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kScore ? kThreadsScore : kThreads, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                   const Params p) {
@@ -597,6 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
   volatile unsigned* arrived = reinterpret_cast<volatile unsigned*>(base_ptr + C::kMiscOff + 8);
 
+  constexpr int kPWarps = kScore ? 16 : 8;  // P/dS warps
+  constexpr int kWarpDq = kPWarps, kWarpTma = kPWarps + 4, kWarpMma = kPWarps + 5;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // Without a window's left bound or a block mask (kMasked = false) those are
@@ -635,14 +654,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // one head after the other. docs, prefix: this batch entry's own.
   const int n_share = kScore ? p.score.group / p.n_seg : 1;
   const int b_of = kScore ? bh / (p.score.H / p.score.group) : 0;
-  const int* const docs =
+  const int* docs =
       (kScore && p.score.docs) ? p.score.docs + static_cast<size_t>(b_of) * (p.score.n_docs + 1)
                                : nullptr;
-  const int* const prefix =
+  const int* prefix =
       (kScore && p.score.prefix) ? p.score.prefix + static_cast<size_t>(b_of) * p.score.n_docs
                                  : nullptr;
   if constexpr (kScore != 0) {
     pdl_wait();  // the offsets may come from the grid before
+    share_documents(reinterpret_cast<int*>(base_ptr + C::kMaskOff), kMaxMaskTiles / 32,
+                    p.score.n_docs, docs, prefix);  // (no block masks here)
     const Span s = query_tiles_of_keys(docs, prefix, p.score.n_docs, p.N, wl, wr, k0);
     i_lo_tile = s.lo;
     i_hi_tile = s.hi;
@@ -674,12 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(bar(C::kBarS + h), 1);
-      mbar_init(bar(C::kBarP + h), 4);        // the 4 warps of half h
+      mbar_init(bar(C::kBarP + h), kPWarps / 2);  // the warps of half h
       mbar_init(bar(C::kBarDQFull + h), 1);
       mbar_init(bar(C::kBarDQEmpty + h), 4);  // the 4 dQ warps
     }
     mbar_init(bar(C::kBarDKDV), 1);
-    mbar_init(bar(C::kBarSplitWritten), 8);  // the 8 P/dS warps
+    mbar_init(bar(C::kBarSplitWritten), kPWarps);
     mbar_init(bar(C::kBarSplitDecided), 1);
     mbar_init(bar(C::kBarDrain), 1);
     *abort_flag = 0;
@@ -822,8 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         FA_TRACE_POINT(2, s, h);
         tc_fence_after();
         const bool acc = (s > 0) || (h > 0);
-        issue_acc_half<D, E>(tmem + C::kTmDV, tm_s + 64 * h, slot_smem(seqO), acc);   // dV
-        issue_acc_half<D, E>(tmem + C::kTmDK, tm_dp + 64 * h, slot_smem(seqQ), acc);  // dK
+        issue_acc_half<D, E, kScore != 0>(tmem + C::kTmDV, tm_s + 64 * h, slot_smem(seqO), acc);   // dV
+        issue_acc_half<D, E, kScore != 0>(tmem + C::kTmDK, tm_dp + 64 * h, slot_smem(seqQ), acc);  // dK
         // dV and dK are the last readers of this half's dO and Q: free their slots
         // before the dQ product, so that the next loads start a product earlier
         tc_commit_e(bar(C::kBarEmpty + slot_of(seqO)));
@@ -850,14 +871,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     drain_wait(bar(C::kBarDrain), 0, p.timeout_ns);
     __syncwarp();
     FA_TRACE_POINT(99, 0, 0);
-  } else if (warp < 8) {
+  } else if (warp < kPWarps) {
     // ------------------------------------------------------------ P^T, dS^T (key rows)
-    const int h = warp >> 2;                  // query half
+    const int h = kScore ? warp >> 3 : warp >> 2;  // query half
+    const int part = kScore ? (warp >> 2) & 1 : 0;  // kScore: which 32 queries of it
     const int krow = (warp & 3) * 32 + lane;  // key row within the tile = TMEM lane
     const int key = k0 + krow;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tm_s = tmem + lane_off + C::kTmS + 64 * h;
-    const uint32_t tm_dp = tmem + lane_off + C::kTmDP + 64 * h;
+    const uint32_t tm_s = tmem + lane_off + C::kTmS + 64 * h + 32 * part;
+    const uint32_t tm_dp = tmem + lane_off + C::kTmDP + 64 * h + 32 * part;
     const float c = p.scale_log2;
     uint8_t* ds_row = base_ptr + C::kDSOff + h * C::kChunkBytes + krow * 128;
     const bool ragged_keys = k0 + BN > p.N;
@@ -902,25 +924,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4* Lv = reinterpret_cast<const float4*>(
           base_ptr + C::kVecOff + slot_of(seqQ) * 2 * C::kVecBytes);
       const float4* Dv4 = Lv + 64 / 4;
-      // masking is needed only where the half crosses an edge of some key's visible
-      // queries (the causal diagonal, a window edge) and on a ragged key tile
-      const bool mask = kScore ? (qh0 < full_lo || qh0 + 64 > full_hi)
-                               : (ragged_keys || (wr >= 0 && k0 + BN - 1 - wr > qh0) ||
-                                  (wl >= 0 && k0 + wl < qh0 + 63));
-      float slope_neg = 0.0f;
-      if constexpr ((kScore & kScoreBias) != 0)
-        slope_neg = -p.score.slopes[bhq % p.score.H] * p.score.slope_mul;
-      const int qoff = qh0 - q_lo;  // query qh0 + x is visible iff qoff + x < q_span (unsigned)
-      // The element loop in two compiled forms: with the mask tests only on steps
-      // that cross a mask edge, none on all the others.
-      if (mask)
-        p_ds_half<E, kDropout, true, kScore>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop,
-                                             lane, qoff, q_span, ds_row, krow, p.score, slope_neg,
-                                             lone - qh0);
-      else
-        p_ds_half<E, kDropout, false, kScore>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop,
-                                              lane, qoff, q_span, ds_row, krow, p.score,
-                                              slope_neg, -1);
+      if constexpr (kScore != 0) {
+        const int q0 = qh0 + 32 * part;  // this thread's 32 queries
+        float slope_neg = 0.0f;
+        if constexpr ((kScore & kScoreBias) != 0)
+          slope_neg = -p.score.slopes[bhq % p.score.H] * p.score.slope_mul;
+        if (q0 < full_lo || q0 + 32 > full_hi)
+          p_ds_quarter<E, true, kScore>(tm_s, tm_dp, Lv + 8 * part, Dv4 + 8 * part, c, key, q0,
+                                        span_bits(q_lo - q0, q_hi - q0), ds_row, krow, 4 * part,
+                                        p.score, slope_neg, lone - q0);
+        else
+          p_ds_quarter<E, false, kScore>(tm_s, tm_dp, Lv + 8 * part, Dv4 + 8 * part, c, key, q0, 0u,
+                                         ds_row, krow, 4 * part, p.score, slope_neg, -1);
+      } else {
+        // masking is needed only where the half crosses an edge of some key's visible
+        // queries (the causal diagonal, a window edge) and on a ragged key tile
+        const bool mask = ragged_keys || (wr >= 0 && k0 + BN - 1 - wr > qh0) ||
+                          (wl >= 0 && k0 + wl < qh0 + 63);
+        const int qoff = qh0 - q_lo;  // query qh0 + x is visible iff qoff + x < q_span (unsigned)
+        // The element loop in two compiled forms: with the mask tests only on steps
+        // that cross a mask edge, none on all the others.
+        if (mask)
+          p_ds_half<E, kDropout, true>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
+                                       qoff, q_span, ds_row, krow);
+        else
+          p_ds_half<E, kDropout, false>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
+                                        qoff, q_span, ds_row, krow);
+      }
       tmem_wait_st();
       fence_proxy_async_smem();
       tc_fence_before();
@@ -929,17 +959,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((warp & 3) == 0) FA_TRACE_POINT(16, s, h);
     }
     if (nsteps == 0 && key < p.N) {
-      // no query sees this key: dK = dV = 0 (warps 0-3 dK, warps 4-7 dV)
+      // no query sees this key: dK = dV = 0 (warps 0-3 dK, warps 4-7 dV; kScore: 0-7 and
+      // 8-15, half the columns each)
+      constexpr int kUnits = kScore ? D / 16 : D / 8;
       uint4* dst = reinterpret_cast<uint4*>((h == 0 ? p.dK : p.dV) +
-                                            (static_cast<size_t>(bh) * p.N + key) * D);
+                                            (static_cast<size_t>(bh) * p.N + key) * D) +
+                   part * kUnits;
 #pragma unroll
-      for (int u = 0; u < D / 8; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
+      for (int u = 0; u < kUnits; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
     }
     if (ok && nsteps > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::kBarDKDV), 0, wd));
     if (threadIdx.x == 0) FA_TRACE_CTA(3);
     if (ok && nsteps > 0) {
-      // warps 0-3 write dK (times scale), warps 4-7 write dV; a split tile's segment
-      // writes its fp32 partial to its slot instead
+      // warps 0-3 write dK (times scale), warps 4-7 write dV (kScore: 0-7 and 8-15, half the
+      // columns each); a split tile's segment writes its fp32 partial to its slot instead
+      constexpr int kColParts = kScore ? D / 64 : D / 32;
+      const int cc_lo = part * kColParts, cc_hi = cc_lo + kColParts;
       tc_fence_after();
       const uint32_t tm_acc = tmem + lane_off + (h == 0 ? C::kTmDK : C::kTmDV);
       uint16_t* out = (h == 0 ? p.dK : p.dV) + (static_cast<size_t>(bh) * p.N + key) * D;
@@ -952,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                static_cast<size_t>(krow) * D;
       };
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
+      for (int cc = cc_lo; cc < cc_hi; ++cc) {
         uint32_t v[32];
         tmem_ld32(tm_acc + cc * 32, v);
         tmem_wait_ld();
@@ -976,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (seg >= 0) {
-        // Count this segment in once all 8 warps' rows are written (bounded waits); the
+        // Count this segment in once all warps' rows are written (bounded waits); the
         // second to arrive adds slot 0 and slot 1, in that order, and writes dK, dV.
         __threadfence();
         __syncwarp();
@@ -995,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float4* s0 = reinterpret_cast<const float4*>(slot_row(0));
           const float4* s1 = reinterpret_cast<const float4*>(slot_row(1));
 #pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
+          for (int cc = cc_lo; cc < cc_hi; ++cc) {
             float4 a[8], b[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -1394,10 +1429,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qoff = qh0 - q_lo;
         if (mask)
           p_ds_half<E, kDropout, true>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
-                                       qoff, q_span, ds_row, krow, p.score, 0.0f, -1);
+                                       qoff, q_span, ds_row, krow);
         else
           p_ds_half<E, kDropout, false>(tm_s, tm_dp, Lv, Dv4, c, key, qh0, ctr_head, p.drop, lane,
-                                        qoff, q_span, ds_row, krow, p.score, 0.0f, -1);
+                                        qoff, q_span, ds_row, krow);
         tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();

@@ -1008,7 +1008,7 @@ template <Elt E, int kScore>
 fa_status launch_bwd_scored(int d, unsigned grid, cudaStream_t s, const CUtensorMap& mq,
                             const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
                             const bwd::Params& p) {
-  constexpr int T = bwd::kThreads;
+  constexpr int T = bwd::kThreadsScore;
   if (d == 64)
     return launch(bwd::fa_bwd_kernel<64, E, true, false, kScore>, grid, T,
                   bwd::Cfg<64>::kSmemBytes, s, mq, mk, mv, mdo, p);
@@ -1115,7 +1115,7 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
   p.n_split = 0;
   p.split_num = 8;
   // the plain backward's rule for the order of the key tiles
-  p.rank_major = (mask.wr >= 0 || mask.wl >= 0) && n_tiles > device_sms() &&
+  p.rank_major = (mask.wr >= 0 || mask.wl >= 0) && n_tiles * p.n_seg > device_sms() &&
                          static_cast<double>(pl.BH) * N * d * 8.0 <= kBwdRankMajorBytes
                      ? 1
                      : 0;

@@ -162,6 +162,21 @@ __device__ __forceinline__ float odd_poly(float s, const float (&q)[n]) {
   return s * r;
 }
 
+// A batch entry's offsets and prefixes copied to shared memory (room for `room` ints) by the
+// whole CTA, where they fit: the searches above are chains of dependent loads, and from global
+// memory they cost a CTA some 5 us before its first tile. docs and prefix are moved to the
+// copy. Every thread of the CTA calls it.
+__device__ __forceinline__ void share_documents(int* shared, int room, int n_docs,
+                                                const int*& docs, const int*& prefix) {
+  const int n = (docs ? n_docs + 1 : 0) + (prefix ? n_docs : 0);
+  if (docs == nullptr || n > room) return;
+  for (int k = threadIdx.x; k < n; k += blockDim.x)
+    shared[k] = k <= n_docs ? docs[k] : prefix[k - n_docs - 1];
+  __syncthreads();
+  docs = shared;
+  if (prefix) prefix = shared + n_docs + 1;
+}
+
 // tanh of one score of any size: 1 - 2 / (1 + e^2x), by the exponential and the reciprocal
 // of the MUFU unit. Absolute error up to 6.3e-7, which the cap multiplies: fit for |x| of the
 // order of one and more, where the polynomials do not reach.

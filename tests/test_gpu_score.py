@@ -88,6 +88,9 @@ CASES = [
                                                  prefix=[[7, 150, 0], [0, 0, 129]], softcap=15.0, slopes=True)),
     (1, 2, 1, 1000, 64, BF, False, (-1, 64), dict(documents=[[128, 384, 896]], prefix=[[256, 256]])),
     (3, 2, 2, 260, 64, BF, True, (-1, -1), dict(documents=[[0, 0], [260, 260], [0, 260]])),
+    # more documents than a CTA keeps in shared memory
+    (1, 2, 1, 620, 64, BF, True, (-1, -1), dict(documents=[list(range(0, 605, 2))], prefix=[[1, 2] * 151])),
+    (2, 2, 2, 200, 128, HF, True, (-1, -1), dict(documents=[list(range(0, 200, 3))] * 2)),
 ]
 
 
