@@ -274,9 +274,10 @@ fa_status fa_backward_dropout_heads(const void* Q, const void* K, const void* V,
  *     h / (H / Hkv), and dK, dV are the sums over the query heads that share it.
  *   softcap: 0 for none, else c > 0 and the scores are capped: c * tanh(scale * q.k / c).
  *     scale / c must lie in [2^-24, 2^12] (else FA_ERR_UNSUPPORTED).
- *   slopes: NULL, or DEVICE memory, fp32 [H]: slopes[h] * |i - j| is subtracted from the
+ *   slopes: NULL, or DEVICE memory, fp32 [H], finite: slopes[h] * |i - j| is subtracted from the
  *     (capped) score of query i and key j. A constant: no gradient for it.
- *   documents: NULL, or DEVICE memory, int32 [B, n_docs + 1], ascending offsets in [0, N]:
+ *   documents: NULL, or DEVICE memory, int32 [B, n_docs + 1] (n_docs <= 2^24), ascending
+ *     offsets in [0, N]:
  *     tokens of batch entry b in [documents[b][m], documents[b][m+1]) are its document m,
  *     and query i sees key j only within one document. Tokens in front of the first offset
  *     or behind the last are padding: they see nothing and nothing sees them (O = 0,
@@ -388,7 +389,10 @@ fa_status fa_cache4_read_f16(void* K, void* V, const void* codes, const void* pa
  *   workspace: fa_cache4_workspace_size(B, H, Hkv, Nq, d, min(max_len, max_pages * page),
  *     window_left) bytes, 16-byte aligned; may be NULL where that is 0. Its contents do not
  *     matter and are undefined on return; calls that may overlap need one each.
- * The result is the same from run to run. Nq = 0 is a no-op.
+ * The result is the same from run to run. Nq = 0 is a no-op. B * H * Nq times the pieces that
+ * a sequence is cut into must stay below 2^31 (else FA_ERR_UNSUPPORTED); the tokens of a
+ * prompt may all be queries, but each 16 rows of a K/V head read the cache again: prompts
+ * are better served by fa_forward_scored over fa_cache4_read.
  */
 fa_status fa_cache4_attend(const void* Q, void* O, float* LSE, const void* codes,
                           const void* params, const int32_t* page_table, const int32_t* lengths,

@@ -903,7 +903,7 @@ fa_status make_score(int B, int H, int Hkv, float scale, float softcap, const fl
   if (H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (!(std::isfinite(softcap) && softcap >= 0.0f)) return FA_ERR_INVALID_ARG;
   if (documents != nullptr && n_docs < 1) return FA_ERR_INVALID_ARG;
-  if (n_docs > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (documents != nullptr && n_docs > (1 << 24)) return FA_ERR_UNSUPPORTED;
   for (const void* p : {static_cast<const void*>(slopes), static_cast<const void*>(documents),
                         static_cast<const void*>(prefix)})
     if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_INVALID_ARG;
@@ -1018,14 +1018,16 @@ fa_status launch_bwd_scored(int d, unsigned grid, cudaStream_t s, const CUtensor
 
 // Segments of the scored backward: CTAs per key tile, each for an equal part of the query heads
 // of its K/V head. Sharing leaves fewer key tiles than SMs on short rows (B3 Hkv2 N1531: 72 of
-// 148); then the group is parted until two waves of CTAs are reached. Each segment writes 256 D
-// fp32 partials and the last one reads them all back, which more CTAs than that do not repay.
+// 148; forward and backward with all score terms 161 us whole, 128 us in four segments); then
+// the group is parted until two waves of CTAs are reached. Each segment writes 256 D fp32
+// partials and the last one reads them all back (about 3 us, as long as a step), which more
+// CTAs than that, or segments of less than two steps, do not repay.
 int score_segments(long long BHkv, int group, int N) {
-  const long long tiles = BHkv * ((static_cast<long long>(N) + 127) / 128);
+  const long long n_kt = (static_cast<long long>(N) + 127) / 128, tiles = BHkv * n_kt;
   int seg = 1;
   if (tiles >= 148) return seg;
   for (int s = 2; s <= group; ++s)
-    if (group % s == 0 && tiles * seg < 2 * 148) seg = s;
+    if (group % s == 0 && tiles * seg < 2 * 148 && n_kt * group >= 2 * s) seg = s;
   return seg;
 }
 
@@ -1241,13 +1243,16 @@ size_t attend_ws_bytes(const AttendPlan& a, int B, int H, int Nq, int d) {
   return round256(slots * d * sizeof(float)) + round256(slots * sizeof(float2));
 }
 
-fa_status check_attend(int B, int H, int Hkv, int Nq, int d, int max_len) {
+fa_status check_attend(int B, int H, int Hkv, int Nq, int d, int max_len, int window_left) {
   if (B < 1 || H < 1 || Hkv < 1 || Nq < 0 || max_len < 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  // row indices and grids stay below 2^31, with up to kAttendFine * kAttendCtas pieces a row
   if (static_cast<long long>(B) * H >= (1ll << 31) || Nq > (1 << 24) ||
-      static_cast<long long>(B) * H * std::max(Nq, 1) >= (1ll << 31) / (kAttendFine * kAttendCtas))
+      static_cast<long long>(B) * H * std::max(Nq, 1) >= (1ll << 31))
     return FA_ERR_UNSUPPORTED;
+  if (Nq == 0) return FA_OK;
+  // rows times pieces, and CTAs (fewer), stay below 2^31
+  const AttendPlan a = attend_plan(B, H, Hkv, Nq, max_len, window_left);
+  if (static_cast<long long>(B) * H * Nq * a.n_pieces >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -1268,7 +1273,7 @@ fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* cod
                              int max_pages, int max_len, float scale, int window_left,
                              float softcap, const float* slopes, void* workspace,
                              size_t workspace_bytes, fa_stream_t stream) {
-  fa_status st = check_attend(B, H, Hkv, Nq, d, max_len);
+  fa_status st = check_attend(B, H, Hkv, Nq, d, max_len, window_left);
   if (st != FA_OK) return st;
   if (!(std::isfinite(scale) && scale > 0.0f)) return FA_ERR_INVALID_ARG;
   cache4::AttendParams p;
@@ -1375,7 +1380,7 @@ fa_status fa_score_span(const int32_t* documents, int n_docs, const int32_t* pre
   if (N < 1 || N > (1 << 30) || index < 0 || index >= N || what < 0 || what > 3 ||
       (causal != 0 && causal != 1) || lo == nullptr || hi == nullptr)
     return FA_ERR_INVALID_ARG;
-  if (documents != nullptr && (n_docs < 1 || n_docs > (1 << 30))) return FA_ERR_INVALID_ARG;
+  if (documents != nullptr && (n_docs < 1 || n_docs > (1 << 24))) return FA_ERR_INVALID_ARG;
   MaskSpec m;
   make_mask(N, causal, window_left, window_right, nullptr, &m);
   if (documents == nullptr) n_docs = 1;
@@ -1711,7 +1716,7 @@ fa_status fa_cache4_attend_f16(const void* Q, void* O, float* LSE, const void* c
 }
 
 size_t fa_cache4_workspace_size(int B, int H, int Hkv, int Nq, int d, int max_len, int window_left) {
-  if (check_attend(B, H, Hkv, Nq, d, max_len) != FA_OK || Nq == 0) return 0;
+  if (check_attend(B, H, Hkv, Nq, d, max_len, window_left) != FA_OK || Nq == 0) return 0;
   return attend_ws_bytes(attend_plan(B, H, Hkv, Nq, max_len, window_left), B, H, Nq, d);
 }
 

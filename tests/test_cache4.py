@@ -79,7 +79,8 @@ def test_cache_calls_refuse_on_the_host(libfa, suffix):
     assert att(lengths=P + 1) == 1 and att(slopes=P + 2) == 1 and att(page=48) == 2
     need = libfa.fa_cache4_workspace_size(2, 4, 2, 1, 64, 65536, -1)
     assert need > 0 and att(nbytes=need - 1) == 1 and att(ws=None) == 1 and att(ws=P + 8) == 1
-    assert att(B=1 << 15, H=1 << 15, Hkv=1) == 2
+    assert att(B=1 << 16, H=1 << 15, Hkv=1) == 2 and att(Nq=1 << 25) == 2
+    assert att(B=1 << 10, H=64, Hkv=1, Nq=1 << 15) == 2  # 2^31 rows
     assert att(Nq=0, Q=None) == 0
 
 
@@ -88,6 +89,8 @@ def test_workspace_size(libfa):
     assert f(1, 8, 8, 1, 64, 127, -1) == 0  # short: one piece a sequence
     assert f(1, 8, 8, 1, 64, 0, -1) == 0
     assert f(1, 8, 3, 1, 64, 4096, -1) == 0 and f(1, 8, 8, 1, 96, 4096, -1) == 0
+    assert f(8, 32, 8, 4096, 128, 4096, -1) == 0  # many rows: sequences stay whole
+    assert f(1, 8, 8, 1, 64, 4096, 2**31 - 1) == f(1, 8, 8, 1, 64, 4096, -1)
     # a window bounds the pieces whatever the length
     assert f(1, 8, 8, 1, 64, 1 << 20, 100) == f(1, 8, 8, 1, 64, 1 << 24, 100)
     assert f(1, 8, 8, 1, 64, 1 << 20, -1) > f(1, 8, 8, 1, 64, 1 << 12, -1) > 0

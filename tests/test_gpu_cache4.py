@@ -123,6 +123,8 @@ CASES = [
     (2, 4, 2, 1, 128, BF, 64, [64, 900], dict(window_left=0)),
     (2, 4, 2, 3, 128, BF, 64, [64, 900], dict(window_left=1000, softcap=10.0, slopes=True)),
     (1, 2, 1, 50, 64, BF, 16, [60], {}),
+    (1, 2, 2, 3, 64, BF, 16, [100], dict(window_left=2**31 - 1)),
+    (2, 2, 1, 40, 64, HF, 16, [30, 90], dict(window_left=2**31 - 2)),
     (1, 4, 1, 1, 128, HF, 128, [9000], dict(slopes=True)),
 ]
 

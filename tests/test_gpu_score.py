@@ -211,6 +211,14 @@ def test_rows_that_see_one_key_have_no_gradient_by_the_scores(N, window, documen
     assert (dq == 0).all() and (dk == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_one_token_without_options(dtype):
+    q, k, v, do = make(2, 3, 3, 1, 64, dtype, seed=1)
+    o, lse = api.forward(q, k, v, causal=True)
+    dq, dk, dv = api.backward(q, k, v, o, lse, do, causal=True)
+    assert torch.equal(o, v) and torch.equal(dv, do) and (dq == 0).all() and (dk == 0).all()
+
+
 @pytest.mark.parametrize("left", [1, 3, 15, 16])
 def test_gradients_of_few_sharp_keys(left):
     """Sharp scores over few keys: dQ and dK within 0.45% in the 2-norm. A model of the

@@ -165,7 +165,9 @@ def test_scored_workspace_size(libfa):
     # of 128 rows in fp32, and a counter per tile
     assert f(3, 8, 2, 1531, 64) == base(3, 8, 1531, 64) + 72 * 4 * 2 * 128 * 64 * 4 + 512
     assert f(2, 16, 4, 4096, 128) == base(2, 16, 4096, 128)  # 256 tiles: whole
-    assert f(1, 6, 1, 128, 64) == base(1, 6, 128, 64) + 6 * 2 * 128 * 64 * 4 + 256
+    # one query tile of 6 heads: 3 segments of two steps
+    assert f(1, 6, 1, 128, 64) == base(1, 6, 128, 64) + 3 * 2 * 128 * 64 * 4 + 256
+    assert f(1, 2, 1, 128, 64) == base(1, 2, 128, 64)  # two steps: whole
     assert f(1, 8, 8, 128, 64) == base(1, 8, 128, 64)  # nothing to part
 
 
