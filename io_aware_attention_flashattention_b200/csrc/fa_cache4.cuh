@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int pos0 = len - p.Nq;  // of the draft's first token
   const int first = p.wl < 0 || p.wl >= pos0 ? 0 : pos0 - p.wl;
   const int g_hi = (len + kGroup - 1) / kGroup;                    // groups with tokens
-  const int s_lo = first / kStep, s_hi = (len + kStep - 1) / kStep;  // steps
+  const int s_lo = first / kStep, s_hi = g_hi / 2 + (g_hi & 1);      // steps
   const int* table = p.L.table + static_cast<size_t>(b) * p.L.max_pages;
 
   // this warp's steps: s_lo + piece * p.piece + warp, every kWarps-th of the piece, then the
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     for (int part = 0; part < 2; ++part) {
       const int grp = 2 * x + part, slot = 2 * buffer + part;
       if (grp < g_hi) {
-        unsigned id = static_cast<unsigned>(__ldg(table + (grp >> page_groups)));
+        unsigned id = static_cast<unsigned>(table[grp >> page_groups]);
         bad &= ~(1u << slot);
         if (id >= n_pages) {
           bad |= 1u << slot;
@@ -466,23 +466,28 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // the queries, as the score product's second operand, and the sums of their channels
+  uint4 qw[NT][D / 32];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = row0 + nt * 8 + g;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w)
+      qw[nt][w] = r < p.rows ? *reinterpret_cast<const uint4*>(p.Q + out_row(r) * D + t * (D / 4) + 8 * w)
+                             : make_uint4(0u, 0u, 0u, 0u);
+  }
   int use = s_lo + piece * p.piece + warp, use_in = 0;
   int ahead = use, ahead_in = 0;
   issue(ahead, 0);
   ahead = next(ahead, ahead_in);
-
-  // the queries, as the score product's second operand, and the sums of their channels
   uint32_t q[NT][KS][2];
   float qs[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = row0 + nt * 8 + g;
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (r < p.rows)
-        x = __ldg(reinterpret_cast<const uint4*>(p.Q + out_row(r) * D + t * (D / 4) + 8 * w));
+      const uint4 x = qw[nt][w];
       const float2 f0 = unpack2<E>(x.x), f1 = unpack2<E>(x.y), f2 = unpack2<E>(x.z),
                    f3 = unpack2<E>(x.w);
       sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       pos[nt][e] = pos0 + (r - h * p.Nq);
       if constexpr ((kMods & kScoreBias) != 0)
         slope_neg[nt][e] =
-            -__ldg(p.score.slopes + hk * group + h) * p.score.slope_mul * p.scale_log2;
+            -p.score.slopes[hk * group + h] * p.score.slope_mul * p.scale_log2;
     }
 
   // Without a cap the scores are in log2 units from the start: c goes into scale and zero.
@@ -628,8 +633,18 @@ __global__ void __launch_bounds__(kWarps * 32)
             for (int e = 0; e < 2; ++e)
               if (key > pos[nt][e] || (p.wl >= 0 && pos[nt][e] - key > p.wl))
                 u[4 * nt + 2 * h + e] = __float_as_uint(-INFINITY);
-          // a token that no row sees has weight 0, whatever its slot holds
-          if (key >= len || (p.wl >= 0 && pos0 - key > p.wl)) vsz[h] = make_float2(0.0f, 0.0f);
+          // A row takes nothing of a token that it does not see, whatever the slot holds, but
+          // its weight of 0 times a NaN would be one: so such a token counts as 0 here, and
+          // makes NaN the rows that see it. (x - x is 0 unless x is an infinity or NaN; zero +
+          // 8 scale is one of them if either part is.)
+          if (vsz[h].y - vsz[h].y != 0.0f) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (__uint_as_float(u[4 * nt + 2 * h + e]) != -INFINITY) z[nt][e] = NAN;
+            vsz[h] = make_float2(0.0f, 0.0f);
+          }
         }
       }
       bool up = false;
@@ -776,8 +791,8 @@ constexpr int kJoinThreads = 512;
 
 template <int D, Elt E>
 __global__ void __launch_bounds__(kJoinThreads)
-    combine_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                   uint16_t* __restrict__ O, float* __restrict__ LSE, int n_pieces) {
+    combine_kernel(const float* part_o, const float2* part_ml, uint16_t* O, float* LSE,
+                   int n_pieces) {
   constexpr int T = D / 4, S = kJoinThreads / T;  // threads of a piece, pieces at a time
   __shared__ float sm_top[kJoinThreads / 32], sm_sum[S];
   __shared__ float4 sm_o[S][T];

@@ -163,6 +163,39 @@ def test_slots_behind_the_length_do_not_matter(dtype):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_draft_tokens_that_a_row_does_not_see(dtype):
+    """NaN in the slot of a draft's later token, or of one that only earlier rows' windows
+    reach: rows that do not see it are as they were."""
+    codes, params, order, g = filled(5, 2, 64, 128, dtype, seed=5)
+    table = order[:4].reshape(1, 4).contiguous()
+    q = torch.randn(1, 8, 3, 128, generator=g, device="cuda").to(dtype)
+    want = check_attend(q, codes, params, table, [201], window_left=50)
+    for token, clean in ((200, slice(0, 2)), (148, slice(1, 3))):  # rows at 198, 199, 200
+        poisoned = params.clone()
+        poisoned[int(table[0, token // 64]), :, :, token % 64] = float("nan")
+        o, _ = api.cache4_attend(q, codes, poisoned, table, dev([201]), scale=1 / math.sqrt(128), window_left=50)
+        assert torch.equal(o[:, :, clean], want[0][:, :, clean])
+        assert torch.isnan(o).any(-1).sum() == 8, "the row that sees it"
+
+
+def test_lengths_near_2_31():
+    """The last tokens of the longest sequence that the interface takes: the same as at the end
+    of a short one."""
+    codes, params, order, g = filled(8, 1, 16, 64, BF, seed=6)
+    long = torch.zeros(1, 2**27 - 1, dtype=torch.int32, device="cuda")
+    long[0, -8:] = order[:8]
+    q = torch.randn(1, 2, 1, 64, generator=g, device="cuda").to(BF)
+    kw = dict(window_left=100, max_len=2**31 - 1)
+    a = api.cache4_attend(q, codes, params, long, dev([2**31 - 16]), **kw)
+    # the same 16 tokens short of a whole step of 32
+    short = torch.zeros(1, 2**6 - 1, dtype=torch.int32, device="cuda")
+    short[0, -8:] = order[:8]
+    b = api.cache4_attend(q, codes, params, short, dev([2**10 - 16]), **kw)
+    assert api.fa_get_status() == 0
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.isfinite(a[1]).all()
+
+
 def test_one_dominant_key_and_large_scores():
     """Scores of hundreds, where the running maximum moves often, and one that wins."""
     codes, params, order, g = filled(40, 1, 16, 128, BF, seed=2)
