@@ -288,7 +288,9 @@ fa_status fa_backward_dropout_heads(const void* Q, const void* K, const void* V,
  *     prefix[b][m] tokens of the document are seen by every query of it, whatever causal
  *     and window_right say (window_left holds for them too). Negative counts as 0.
  *   causal, window_left, window_right: as for fa_forward_masked.
- * The tensors must be finite at padding positions as well (weights of 0 multiply them).
+ * Padding positions may hold anything, NaN included. Tokens of documents must be finite:
+ * documents that meet inside a tile of 128 share its products, where a weight of 0 meets
+ * the other's values.
  * n_docs is not read without documents. Workspace: fa_backward_scored_workspace_size bytes;
  * fa_backward_workspace_size(B, H, N, d) is enough to run, but where key tiles are few it may
  * leave no room to part the query heads of a K/V head over several CTAs (dK and dV then
@@ -353,7 +355,8 @@ fa_status fa_score_span(const int32_t* documents, int n_docs, const int32_t* pre
  * status word: fa_get_status() then returns FA_ERR_BAD_PAGE.
  *
  * fa_cache4_append: K, V [B, Hkv, n, d] into the cache: token t < counts[b] of sequence b
- *   goes to position positions[b] + t. counts (DEVICE int32 [B]) may be NULL: n each; larger
+ *   goes to position positions[b] + t. No two tokens of a call may share a slot (which would
+ *   win is open, and codes and pair may come from different ones). counts (DEVICE int32 [B]) may be NULL: n each; larger
  *   counts count as n. Nothing else of the cache changes. Rows must be finite: a row with
  *   a NaN reads back as NaN, one with an infinity has undefined values.
  * fa_cache4_read: the same rows back, into K, V [B, Hkv, n, d]; rows t >= counts[b] are 0.

@@ -412,10 +412,11 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_scored_kernel(const PreParams 
       weight += __shfl_xor_sync(0xffffffffu, weight, o2);
       acc += __shfl_xor_sync(0xffffffffu, acc, o2);
     }
-    if (lane == 0) few_d[f] = acc / weight;
+    if (lane == 0) few_d[f] = weight == 0.0f ? 0.0f : acc / weight;
   }
   __syncthreads();
   if (mine >= 0) d = few_d[mine];
+  if (ks.hi <= ks.lo) d = 0.0f;  // padding may hold NaN
   if (lane < kRows) {
     p.L2[r + lane] = l2;
     p.Dv[r + lane] = d;
@@ -811,6 +812,15 @@ __global__ void __launch_bounds__(kScore ? kThreadsScore : kThreads, 1)
     const uint32_t ds_smem = base + C::kDSOff;
     const uint32_t tm_s = tmem + C::kTmS, tm_dp = tmem + C::kTmDP;
     bool ok = mbar_wait_warp(bar(C::kBarKV), 0, wd);
+    [[maybe_unused]] Span real{0, 0};  // kScore: the rows that are not padding
+    [[maybe_unused]] int qi = i_lo;    // kScore: the query tile of the next issue_sdp
+    if constexpr (kScore != 0) {
+      real = padding_bounds(docs, p.score.n_docs, p.N);
+      if (nsteps > 0) {
+        zero_padding<D>(base_ptr + C::kKOff, C::kChunkBytes, BN, k0, real);
+        zero_padding<D>(base_ptr + C::kVOff, C::kChunkBytes, BN, k0, real);
+      }
+    }
     auto wait_full = [&](int seq) -> bool {
       return mbar_wait_warp(bar(C::kBarFull + slot_of(seq)), round_of(seq) & 1, wd);
     };
@@ -820,6 +830,11 @@ __global__ void __launch_bounds__(kScore ? kThreadsScore : kThreads, 1)
         const int seqO = seq_of(s, h, 0), seqQ = seq_of(s, h, 1);
         if (!(wait_full(seqO) && wait_full(seqQ))) return false;
         FA_TRACE_POINT(5, s, h);
+        if (kScore != 0 && (qi * BM + 64 * h < real.lo || qi * BM + 64 * h + 64 > real.hi))
+#pragma unroll 1
+          for (int seq = seqO; seq <= seqQ; seq += seqQ - seqO)
+            zero_padding<D>(base_ptr + C::kRingOff + slot_of(seq) * C::kHalfBytes,
+                            C::kHalfChunkBytes, 64, qi * BM + 64 * h, real);
         tc_fence_after();
         issue_xyT_half<D, E>(tm_dp + 64 * h, v_smem, slot_smem(seqO));
         if (D == 128 && s > 0) {  // S^T_h shares columns with dQ^T_h of the last step
@@ -832,6 +847,7 @@ __global__ void __launch_bounds__(kScore ? kThreadsScore : kThreads, 1)
         FA_TRACE_POINT(8, s, h);
         if (s == 0 && h == 0 && lane == 0) FA_TRACE_CTA(2);
       }
+      if (kScore != 0 && ++qi >= i_hi) qi = i_lo;
       return true;
     };
     if (ok && nsteps > 0) ok = issue_sdp(0);

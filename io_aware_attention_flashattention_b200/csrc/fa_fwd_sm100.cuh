@@ -759,6 +759,8 @@ __global__ void __launch_bounds__(kScore ? kThreadsScore : kThreads, 1)
     auto wait_v = [&](int j) {
       return mbar_wait_warp(bar(C::kBarVFull + j % C::kVSlots), (j / C::kVSlots) & 1, wd);
     };
+    [[maybe_unused]] Span real{0, 0};  // kScore: the rows that are not padding
+    if constexpr (kScore != 0) real = padding_bounds(docs, p.score.n_docs, p.N);
     // ns[t] / npv[t]: S_t and PV_t products issued so far (their barrier phases)
     int ns[2] = {0, 0}, npv[2] = {0, 0};
     // S_t for the key tile at ring index j, for each query tile that sees it, each
@@ -801,6 +803,9 @@ __global__ void __launch_bounds__(kScore ? kThreadsScore : kThreads, 1)
         if (!have_v) {
           if (!wait_v(j)) { ok = false; break; }
           FA_TRACE_POINT(48, j, 0);
+          if constexpr (kScore != 0)
+            zero_padding<D>(base_ptr + C::kVOff + (j % C::kVSlots) * C::kTileBytes, C::kChunkBytes,
+                            BN, cur * BN, real);
           have_v = true;
         }
         tc_fence_after();

@@ -931,6 +931,7 @@ fa_status make_score(int B, int H, int Hkv, float scale, float softcap, const fl
     s->cap_in2 = static_cast<float>(2.0 * 1.4426950408889634 * a);
   }
   s->slope_mul = softcap > 0.0f ? 1.0f / softcap : 1.0f / scale;
+  if (slopes != nullptr && !std::isfinite(s->slope_mul)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 

@@ -119,6 +119,13 @@ __host__ __device__ __forceinline__ void real_rows(const int* docs, int n_docs, 
   }
 }
 
+// Rows [lo, hi) hold the tokens of documents; the others are padding. The bounds of tests that
+// no row of a tile meets where there is no padding (rows from N on read as zeros).
+__device__ __forceinline__ Span padding_bounds(const int* docs, int n_docs, int N) {
+  if (docs == nullptr) return Span{0, 0x7fffffff};
+  return Span{docs[0], docs[n_docs] >= N ? 0x7fffffff : docs[n_docs]};
+}
+
 // 128-wide tiles [lo, hi) that hold every key some query of rows [r0, r0 + 127] sees.
 __host__ __device__ __forceinline__ Span key_tiles_of_rows(const int* docs, const int* prefix,
                                                            int n_docs, int N, int wl, int wr,
@@ -143,6 +150,32 @@ __host__ __device__ __forceinline__ Span query_tiles_of_keys(const int* docs, co
   const Span b = queries_of_key(docs, prefix, n_docs, N, wl, wr, last);
   if (b.hi <= a.lo) return Span{0, 0};
   return Span{a.lo / 128, (b.hi + 127) / 128};
+}
+
+// Rows of a tile in shared memory (D / 64 chunks of 128-byte rows, `first` the first row's
+// token) that are padding, made zeros by one warp before the products that read them: the
+// weights of padding are 0, but times a NaN there they would be NaN. Called by the warp that
+// issues the products, once the tile has landed. Few tiles hold padding, and inlined into the
+// issuer's loop these stores slowed every step of the backward (B1 H8 N16384 d128 by 3%, with
+// no documents at all; B2 H16 Hkv4 N4096 in documents by 9%, as a call by 4%).
+template <int D>
+__device__ __noinline__ void zero_rows(uint8_t* tile, int chunk_bytes, int rows, int first, int lo,
+                                       int hi) {
+  for (int u = threadIdx.x & 31; u < rows * 8; u += 32) {
+    const int at = first + u / 8;
+    if (at < lo || at >= hi)
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        *reinterpret_cast<uint4*>(tile + c * chunk_bytes + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+template <int D>
+__device__ __forceinline__ void zero_padding(uint8_t* tile, int chunk_bytes, int rows, int first,
+                                             const Span& real) {
+  if (first < real.lo || first + rows > real.hi)
+    zero_rows<D>(tile, chunk_bytes, rows, first, real.lo, real.hi);
 }
 
 // s * q(S) for a pair of scores, on the FMA pipe, with S = s * s.

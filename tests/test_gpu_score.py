@@ -106,6 +106,39 @@ def test_forward_and_backward(case):
     check(got, q, k, v, do, mask, scale, rest.get("softcap"), kw.get("slopes"))
 
 
+@pytest.mark.parametrize("dtype,d,H,Hkv,causal,softcap,slopes", [
+    (BF, 128, 2, 2, True, None, False), (HF, 64, 4, 1, False, 20.0, True), (BF, 64, 6, 2, True, 50.0, False),
+    (HF, 128, 4, 2, False, None, True)])
+def test_padding_may_hold_anything(dtype, d, H, Hkv, causal, softcap, slopes):
+    """NaN and infinities in front of the first document and behind the last, in q, k, v, o and
+    do: the results are those of clean tensors, zeros at the padding."""
+    B, N = 3, 500
+    docs = [[0, 100, 301], [37, 200, 431], [130, 130, 380]]
+    q, k, v, do = make(B, H, Hkv, N, d, dtype, seed=d + H)
+    kw = options(dict(documents=docs, slopes=slopes), B, H, N)
+    if softcap:
+        kw["softcap"] = softcap
+    scale = 1.0 / math.sqrt(d)
+    bad = [x.clone() for x in (q, k, v, do)]
+    for b, cuts in enumerate(docs):
+        for x in bad:
+            for c, fill in ((slice(0, cuts[0]), math.nan), (slice(cuts[-1], N), math.inf)):
+                x[b, :, c] = fill
+                x[b, :, c, ::3] = math.nan
+    mask = ref.visible(B, N, causal, documents=docs)
+    got = run(*bad, scale, causal, None, kw)
+    check(got, q, k, v, do, mask, scale, softcap, kw.get("slopes"))
+    suffix = "_f16" if dtype == HF else ""
+    o, lse = got[0].clone(), got[1]
+    for b, cuts in enumerate(docs):
+        o[b, :, :cuts[0]] = o[b, :, cuts[-1]:] = math.nan
+    grads = [torch.full_like(x, math.nan) for x in (q, k, v)]
+    ws = torch.full((api.fa_backward_scored_workspace_size(B, H, Hkv, N, d),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    getattr(api, "fa_backward_scored" + suffix)(*bad[:3], o, bad[3], lse, *grads, scale, causal, ws, None, **kw)
+    check((got[0], lse, *grads), q, k, v, do, mask, scale, softcap, kw.get("slopes"))
+
+
 @pytest.mark.parametrize("H,Hkv", [(6, 1), (8, 2), (4, 4)])
 def test_segments_of_a_group(H, Hkv):
     """Key tiles run by several CTAs, a part of the group's heads each: the same from run to
