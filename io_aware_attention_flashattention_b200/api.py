@@ -30,7 +30,8 @@ __all__ = [
     "fa_backward_masked", "fa_forward_dropout", "fa_backward_dropout", "fa_forward_f32",
     "fa_backward_f32", "fa_forward_scored", "fa_backward_scored", "fa_forward_scored_f16",
     "fa_backward_scored_f16", "fa_cache4_append", "fa_cache4_read", "fa_cache4_attend",
-    "fa_cache4_append_f16", "fa_cache4_read_f16", "fa_cache4_attend_f16", "fa_get_status", "fa_watchdog_selftest", "fa_version", "fa_dropout_rate",
+    "fa_cache4_append_f16", "fa_cache4_read_f16", "fa_cache4_attend_f16",
+    "fa_get_status", "fa_watchdog_selftest", "fa_version", "fa_dropout_rate",
     "fa_launch_plan",
     "forward", "backward", "attention", "FlashAttentionFunction", "cache4_empty",
     "cache4_append", "cache4_read", "cache4_attend",
@@ -167,11 +168,16 @@ def _block_mask(block_mask, N: int):
     return block_mask.data_ptr()
 
 
+def _bound(n) -> int:
+    """A window's side as the library takes it: 32 bits, -1 for none."""
+    return max(-1, min(int(n), 2**31 - 1))
+
+
 def _window(window):
     if window is None:
         return -1, -1
     left, right = window
-    return int(left), int(right)
+    return _bound(left), _bound(right)
 
 
 @_on_one_device
@@ -506,7 +512,7 @@ def _cache4_attend(name, dtype, Q, O, LSE, codes, params, page_table, lengths, m
     ws, nbytes = (None, 0) if workspace is None else _ws(workspace)
     check(name, getattr(lib(), name)(
         *qo, *ptrs, _need("lengths", lengths, torch.int32, (B,)), B, H, Hkv, Nq, d, page, n_pages,
-        max_pages, int(max_len), float(scale), int(window_left),
+        max_pages, int(max_len), float(scale), _bound(window_left),
         0.0 if softcap is None else float(softcap),
         _device_array("slopes", slopes, torch.float32, (H,)), ws, nbytes, _stream(stream)))
 
@@ -776,6 +782,7 @@ def cache4_attend(q, codes, params, page_table, lengths, scale=None, window_left
     max_len = room if max_len is None else min(int(max_len), room)
     o = torch.empty_like(q)
     lse = q.new_empty((B, H, n), dtype=torch.float32)
+    window_left = _bound(window_left)
     nbytes = fa_cache4_workspace_size(B, H, codes.shape[2], n, d, max_len, window_left)
     ws = q.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
     _cache4_attend("fa_cache4_attend" + _cache4_suffix(q.dtype), q.dtype, q, o, lse, codes, params,

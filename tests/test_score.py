@@ -190,3 +190,10 @@ def test_binding_refuses_what_does_not_combine():
         api.attention(q, k, k, slopes=torch.ones(4, requires_grad=True))
     with pytest.raises(ValueError, match="offsets"):
         api._score(1, 4, None, None, torch.zeros(3, dtype=torch.int32), None)
+
+
+def test_binding_holds_windows_to_32_bits():
+    from io_aware_attention_flashattention_b200 import api
+
+    assert api._window((2**40, 2**32)) == (2**31 - 1, 2**31 - 1)
+    assert api._window((-2**40, 5)) == (-1, 5) and api._window(None) == (-1, -1)
