@@ -97,7 +97,7 @@ def lib() -> ctypes.CDLL:
                     f"{LIB} is missing: build it with "
                     "`python -m io_aware_attention_flashattention_b200.build`")
             h = ctypes.CDLL(LIB)
-            # (_handle is set only once every signature is)
+            # _handle is read above without the lock, so it is set last, with every signature in place.
             for name, (res, args) in SIGNATURES.items():
                 fn = getattr(h, name)
                 fn.restype = res

@@ -44,6 +44,12 @@
 // keys, and elements are masked only on steps that cross a window edge. A key tile
 // that no query sees gets dK = dV = 0.
 // No N x N matrix is written to device memory.
+//
+// Shaped scores (kScore != 0, 704 threads): the preprocess is fa_bwd_pre_scored_kernel; a CTA
+// owns a key tile of a K/V head and walks the query tiles of every head that shares it (or
+// of a part of them: segments, joined in order); warps 8h..8h+7 form P^T and dS^T of half h,
+// two threads a key row (p_ds_quarter); the dQ warps, producer and issuer follow as warps
+// 16-21.
 #pragma once
 
 #include <type_traits>

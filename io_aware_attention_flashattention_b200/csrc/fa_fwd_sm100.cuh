@@ -37,6 +37,11 @@
 //     2^8 (exact: O and l always share the same reference max).
 //   * TMEM: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D).
 //   * Epilogue: O/l rounded to bf16 stored row per thread; LSE = (m + log2 l) ln 2.
+//
+// Shaped scores (kScore != 0, 608 threads): the key tiles come from the documents and prefixes
+// (fa_score.cuh), K and V from the head that the query head's group shares, and warps 0-7 /
+// 8-15 are the softmax of tile 0 / 1, two threads a row (scored_half_tile); the producers and
+// the issuer follow them as warps 16-18.
 #pragma once
 
 #include "fa_ptx.cuh"

@@ -196,9 +196,10 @@ __device__ __forceinline__ float odd_poly(float s, const float (&q)[n]) {
 }
 
 // A batch entry's offsets and prefixes copied to shared memory (room for `room` ints) by the
-// whole CTA, where they fit: the searches above are chains of dependent loads, and from global
-// memory they cost a CTA some 5 us before its first tile. docs and prefix are moved to the
-// copy. Every thread of the CTA calls it.
+// whole CTA, where they fit: the searches above are chains of dependent loads. docs and prefix
+// are moved to the copy. Every thread of the CTA calls it. In the backward, together with
+// key tiles ordered by rank, it took forward and backward at B3 H8 Hkv2 N1531 d64 (5
+// documents a row) from 128 to 122 us; the forward gained nothing by it and searches in place.
 __device__ __forceinline__ void share_documents(int* shared, int room, int n_docs,
                                                 const int*& docs, const int*& prefix) {
   const int n = (docs ? n_docs + 1 : 0) + (prefix ? n_docs : 0);

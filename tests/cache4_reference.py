@@ -32,8 +32,9 @@ def rows(codes, params, table_row, length):
 def attend(q, codes, params, table, lengths, scale, window_left=-1, softcap=None, slopes=None, gone=()):
     """((o, lse), bounds) in 64 bits. gone: pairs (sequence, page index) that hold nothing.
 
-    The bounds: a score is d products q * (16 + code) summed in 32 bits, times the scale, plus
-    the zero's part: off by 2^-23 (d + 8) sum|q| (31 scale + |zero|) and, as any shaped score,
+    The bounds: a score is d products q * (code - 8) summed in 32 bits, times the scale, plus
+    sum q times zero + 8 scale: off by at most 2^-23 (d + 8) sum|q| (16 scale + |zero|), and
+    31 for 16 leaves room for codes that are not centred; and, as any shaped score,
     8 * 2^-23 (|t| + cap + 1). The weights times the value's scale are rounded to bf16 (2^-8)
     before they meet code - 8, the sums over L tokens are in 32 bits (L * 2^-23 of what is
     summed), and the output is rounded to its type."""
