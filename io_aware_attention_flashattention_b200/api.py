@@ -40,6 +40,7 @@ __all__ = [
 
 _Tensor, _Stream = torch.Tensor, torch.cuda.Stream
 _current_device = torch.cuda.current_device
+_current_gpu = torch._C._cuda_getDevice  # the same without initialising CUDA: a GPU tensor has
 
 
 def _one_device(*args):
@@ -74,7 +75,7 @@ def _on_one_device(fn):
                     break
                 index = i
         else:
-            if index < 0 or index == _current_device():
+            if index < 0 or index == _current_gpu():
                 return fn(*args, **kwargs)
         with _one_device(*args, *kwargs.values()):
             return fn(*args, **kwargs)
@@ -170,7 +171,8 @@ def _block_mask(block_mask, N: int):
 
 def _bound(n) -> int:
     """A window's side as the library takes it: 32 bits, -1 for none."""
-    return max(-1, min(int(n), 2**31 - 1))
+    n = int(n)
+    return n if -1 <= n < 2**31 else max(-1, min(n, 2**31 - 1))
 
 
 def _window(window):
@@ -404,6 +406,8 @@ def _device_array(name, t, dtype, shape):
 
 def _score(B, H, softcap, slopes, documents, prefix):
     """The C arguments softcap, slopes, documents, n_docs, prefix."""
+    if slopes is None and documents is None and prefix is None:
+        return 0.0 if softcap is None else float(softcap), None, None, 1, None
     n_docs = 1
     if documents is not None:
         if documents.dim() != 2 or documents.shape[1] < 2:
@@ -421,13 +425,15 @@ def _score(B, H, softcap, slopes, documents, prefix):
 def _forward_scored(name, dtype, Q, K, V, O, LSE, scale, causal, window, softcap, slopes,
                     documents, prefix, stream):
     B, H, Hkv, N, d = _shared_heads(Q, K)
-    args = [_need("Q", Q, dtype, (B, H, N, d)), _need("K", K, dtype, (B, Hkv, N, d)),
-            _need("V", V, dtype, (B, Hkv, N, d)), _need("O", O, dtype, (B, H, N, d)),
-            _need("LSE", LSE, torch.float32, (B, H, N))]
+    sq, sk = (B, H, N, d), (B, Hkv, N, d)
+    args = (_need("Q", Q, dtype, sq), _need("K", K, dtype, sk), _need("V", V, dtype, sk),
+            _need("O", O, dtype, sq), _need("LSE", LSE, torch.float32, (B, H, N)))
     wl, wr = _window(window)
-    check(name, getattr(lib(), name)(
+    status = getattr(lib(), name)(
         *args, B, H, Hkv, N, d, float(scale), int(bool(causal)), wl, wr,
-        *_score(B, H, softcap, slopes, documents, prefix), _stream(stream)))
+        *_score(B, H, softcap, slopes, documents, prefix), _stream(stream))
+    if status:
+        check(name, status)
 
 
 def _backward_scored(name, dtype, Q, K, V, O, dO, LSE, dQ, dK, dV, scale, causal, workspace,
@@ -493,28 +499,32 @@ def _cache4(codes, params, page_table, dtype, B, Hkv, d):
 
 
 def _cache4_rows(name, dtype, K, V, codes, params, page_table, positions, counts, stream):
-    B, Hkv, n, d = _shape(K)
-    kv = (_need("K", K, dtype, (B, Hkv, n, d)), _need("V", V, dtype, (B, Hkv, n, d)))
+    shape = B, Hkv, n, d = _shape(K)
+    k, v = _need("K", K, dtype, shape), _need("V", V, dtype, shape)
     ptrs, sizes = _cache4(codes, params, page_table, dtype, B, Hkv, d)
-    check(name, getattr(lib(), name)(
-        *kv, *ptrs, _need("positions", positions, torch.int32, (B,)),
-        _device_array("counts", counts, torch.int32, (B,)), B, Hkv, n, d, *sizes,
-        _stream(stream)))
+    status = getattr(lib(), name)(
+        k, v, *ptrs, _need("positions", positions, torch.int32, (B,)),
+        None if counts is None else _need("counts", counts, torch.int32, (B,)), B, Hkv, n, d, *sizes,
+        _stream(stream))
+    if status:
+        check(name, status)
 
 
 def _cache4_attend(name, dtype, Q, O, LSE, codes, params, page_table, lengths, max_len, scale,
                    window_left, softcap, slopes, workspace, stream):
-    B, H, Nq, d = _shape(Q)
-    Hkv = int(codes.shape[2]) if codes.dim() == 5 else 0
-    qo = (_need("Q", Q, dtype, (B, H, Nq, d)), _need("O", O, dtype, (B, H, Nq, d)),
-          _need("LSE", LSE, torch.float32, (B, H, Nq)))
-    ptrs, (page, n_pages, max_pages) = _cache4(codes, params, page_table, dtype, B, Hkv, d)
+    shape = B, H, Nq, d = _shape(Q)
+    Hkv = codes.shape[2] if codes.dim() == 5 else 0
+    q, o = _need("Q", Q, dtype, shape), _need("O", O, dtype, shape)
+    lse = _need("LSE", LSE, torch.float32, (B, H, Nq))
+    ptrs, sizes = _cache4(codes, params, page_table, dtype, B, Hkv, d)
     ws, nbytes = (None, 0) if workspace is None else _ws(workspace)
-    check(name, getattr(lib(), name)(
-        *qo, *ptrs, _need("lengths", lengths, torch.int32, (B,)), B, H, Hkv, Nq, d, page, n_pages,
-        max_pages, int(max_len), float(scale), _bound(window_left),
-        0.0 if softcap is None else float(softcap),
-        _device_array("slopes", slopes, torch.float32, (H,)), ws, nbytes, _stream(stream)))
+    status = getattr(lib(), name)(
+        q, o, lse, *ptrs, _need("lengths", lengths, torch.int32, (B,)), B, H, Hkv, Nq, d, *sizes,
+        int(max_len), float(scale), _bound(window_left), 0.0 if softcap is None else float(softcap),
+        None if slopes is None else _need("slopes", slopes, torch.float32, (H,)), ws, nbytes,
+        _stream(stream))
+    if status:
+        check(name, status)
 
 
 @_on_one_device
@@ -599,10 +609,12 @@ def _check_scored(q, block_mask, dropout) -> str:
     if block_mask is not None or dropout is not None:
         raise ValueError("block_mask and dropout do not combine with softcap, slopes, documents, "
                          "prefix or shared K/V heads")
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    if q.dtype is torch.bfloat16:
+        return ""
+    if q.dtype is not torch.float16:
         raise TypeError("softcap, slopes, documents, prefix and shared K/V heads are supported "
                         "for bf16 and f16 inputs")
-    return "" if q.dtype == torch.bfloat16 else "_f16"
+    return "_f16"
 
 
 def forward(q, k, v, causal: bool = False, scale=None, window=None, block_mask=None,
@@ -724,7 +736,11 @@ def attention(q, k, v, causal: bool = False, scale=None, window=None, block_mask
               dropout=None, softcap=None, slopes=None, documents=None, prefix=None):
     """Differentiable attention; ``dropout`` = (p, seed, offset): pass a new offset (or
     seed) per call to draw a new mask. ``softcap``, ``slopes``, ``documents`` and
-    ``prefix`` as for ``forward``; slopes are constants (no gradient)."""
+    ``prefix`` as for ``forward``; slopes are constants (no gradient).
+
+    A backward pass may be captured into a CUDA graph, but not while an eager graph of the same
+    leaves is alive (drop its outputs first): autograd would tie the captured pass to the
+    eager one's stream, which ends the process."""
     return FlashAttentionFunction.apply(q, k, v, causal, scale, window, block_mask, dropout,
                                         softcap, slopes, documents, prefix)
 
@@ -733,9 +749,11 @@ def attention(q, k, v, causal: bool = False, scale=None, window=None, block_mask
 
 
 def _cache4_suffix(dtype) -> str:
-    if dtype not in (torch.bfloat16, torch.float16):
+    if dtype is torch.bfloat16:
+        return ""
+    if dtype is not torch.float16:
         raise TypeError(f"the 4-bit cache serves bf16 and f16 models, not {dtype}")
-    return "" if dtype == torch.bfloat16 else "_f16"
+    return "_f16"
 
 
 def cache4_empty(n_pages: int, kv_heads: int, page: int, d: int, dtype=torch.bfloat16,
