@@ -317,16 +317,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // Nibbles j of both halves of a word as a pair of 16-bit floats code - 8: 128 + code (bf16) or
-// 1024 + code (f16), the code being the mantissa's last bits, and one exact addition.
+// 1024 + code (f16), the code being the mantissa's last bits, and one exact addition. The
+// mantissa of f16 has room for the nibble four bits up as well: 1024 + 16 code, and one
+// exact multiplication and addition, which spares the shift (f16 B1 H32 Hkv4 L131071 31.9 ->
+// 31.5 us).
 template <Elt E, int j>
 __device__ __forceinline__ uint32_t centred(uint32_t w) {
   uint32_t r;
   if constexpr (E == Elt::BF16)
     asm("add.rn.bf16x2 %0, %1, %2;"
         : "=r"(r) : "r"(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u)), "r"(0xC308C308u));
-  else
+  else if constexpr (j % 2 == 0)
     asm("add.rn.f16x2 %0, %1, %2;"
         : "=r"(r) : "r"(and_or(w >> (4 * j), 0x000F000Fu, 0x64006400u)), "r"(0xE408E408u));
+  else  // / 16 - 72
+    asm("fma.rn.f16x2 %0, %1, %2, %3;"
+        : "=r"(r) : "r"(and_or(w >> (4 * j - 4), 0x00F000F0u, 0x64006400u)), "r"(0x2C002C00u),
+                    "r"(0xD480D480u));
   return r;
 }
 
