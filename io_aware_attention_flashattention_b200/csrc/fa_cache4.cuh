@@ -376,12 +376,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   constexpr int kHalf = kGroup * kRow;      // of a group's K or V codes
   constexpr int kPart = 2 * kHalf + 2 * kGroup * 4;  // of a group: codes, then the pairs
   constexpr int kRing = kWarps * 4 * kPart;
-  constexpr int kJoin = kWarps * R * (D + 4 + 2) * 4;
+  constexpr int kJoin = kWarps * 8 * (D + 4 + 2) * 4;
   // the buffers, and after the loop the warps' results
   __shared__ __align__(128) uint8_t smem[kRing > kJoin ? kRing : kJoin];
-  float (*const sm_o)[R][D + 4] = reinterpret_cast<float (*)[R][D + 4]>(smem);
-  float (*const sm_m)[R] = reinterpret_cast<float (*)[R]>(smem + kWarps * R * (D + 4) * 4);
-  float (*const sm_l)[R] = reinterpret_cast<float (*)[R]>(smem + kWarps * R * (D + 5) * 4);
+  float (*const sm_o)[8][D + 4] = reinterpret_cast<float (*)[8][D + 4]>(smem);
+  float (*const sm_m)[8] = reinterpret_cast<float (*)[8]>(smem + kWarps * 8 * (D + 4) * 4);
+  float (*const sm_l)[8] = reinterpret_cast<float (*)[8]>(smem + kWarps * 8 * (D + 5) * 4);
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -732,11 +732,13 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();  // the ring is free
 
-  // this warp's rows into shared memory: row 2t + e, channels g * D / 8 + 8w + 2i + (0, 1)
+  // The warps' rows joined, eight at a time: a warp's row 2t + e, channels g * D / 8 + 8w + 2i +
+  // (0, 1), into shared memory, then D / 4 threads a row.
+  constexpr int T = D / 4;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
+    __syncthreads();  // the ring, or the eight rows before, are free
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -744,7 +746,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
         z[nt][e] += __shfl_xor_sync(0xffffffffu, z[nt][e], d);
       }
-      const int r = nt * 8 + 2 * t + e;
+      const int r = 2 * t + e;
       if (g == 0) {
         sm_m[warp][r] = bound[nt][e] == -INFINITY ? -INFINITY : m[nt][e];
         sm_l[warp][r] = l[nt][e];
@@ -754,38 +756,38 @@ __global__ void __launch_bounds__(kWarps * 32)
         *reinterpret_cast<float2*>(&sm_o[warp][r][g * (D / 8) + 2 * mt]) =
             make_float2(o[nt][mt][e] + z[nt][e], o[nt][mt][2 + e] + z[nt][e]);
     }
-  __syncthreads();
-  // the warps' rows joined: D / 4 threads a row
-  constexpr int T = D / 4;
-  for (int r = threadIdx.x / T; r < n_rows; r += kWarps * 32 / T) {
-    const int ch = (threadIdx.x % T) * 4;
-    float top = sm_m[0][r];
+    __syncthreads();
+    const int here = min(8, n_rows - 8 * nt);
+    for (int r = threadIdx.x / T; r < here; r += kWarps * 32 / T) {
+      const int ch = (threadIdx.x % T) * 4;
+      float top = sm_m[0][r];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][r]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][r]);
+      const float base = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2_approx(sm_m[w][r] - base);
-      const float4 v = *reinterpret_cast<const float4*>(&sm_o[w][r][ch]);
-      sum = fmaf(f, sm_l[w][r], sum);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
-    }
-    const size_t row = out_row(row0 + r);
-    if (p.n_pieces > 1) {
-      const size_t slot = row * p.n_pieces + piece;
-      if (ch == 0) p.part_ml[slot] = make_float2(top, sum);
-      if (sum > 0.0f || sum != sum) *reinterpret_cast<float4*>(p.part_o + slot * D + ch) = acc;
-    } else {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      *reinterpret_cast<uint2*>(p.O + row * D + ch) =
-          make_uint2(pack2<E>(acc.x * inv, acc.y * inv), pack2<E>(acc.z * inv, acc.w * inv));
-      if (ch == 0)
-        p.LSE[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2_approx(sm_m[w][r] - base);
+        const float4 v = *reinterpret_cast<const float4*>(&sm_o[w][r][ch]);
+        sum = fmaf(f, sm_l[w][r], sum);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      const size_t row = out_row(row0 + 8 * nt + r);
+      if (p.n_pieces > 1) {
+        const size_t slot = row * p.n_pieces + piece;
+        if (ch == 0) p.part_ml[slot] = make_float2(top, sum);
+        if (sum > 0.0f || sum != sum) *reinterpret_cast<float4*>(p.part_o + slot * D + ch) = acc;
+      } else {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        *reinterpret_cast<uint2*>(p.O + row * D + ch) =
+            make_uint2(pack2<E>(acc.x * inv, acc.y * inv), pack2<E>(acc.z * inv, acc.w * inv));
+        if (ch == 0)
+          p.LSE[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+      }
     }
   }
 }

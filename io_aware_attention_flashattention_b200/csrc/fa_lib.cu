@@ -1203,8 +1203,12 @@ fa_status cache4_rows_impl(const void* K, const void* V, void* codes, void* para
   }
 }
 
-// How an attend call is cut: query rows per CTA (8 or 16), pieces of a sequence and steps of
-// 32 tokens per piece, from the bound on the lengths that the caller gives.
+// How an attend call is cut: query rows per CTA (8, 16 or 24), pieces of a sequence and steps of
+// 32 tokens per piece, from the bound on the lengths that the caller gives. 24 rows take
+// 254 registers (two CTAs an SM; 16 take 168, three) and pay only where they spare a second
+// pass over the cache. In passes of 16 / of 24, d = 128: 20 rows B64 Hkv8 L4096 276 / 222 us, B8
+// Hkv4 L2048 18.1 / 14.4 us; 40 rows B32 Hkv4 L4096 124 / 127 us, B1 Hkv4 L32768 30 / 33 us; 48
+// rows B32 Hkv8 L4096 228 / 228 us.
 struct AttendPlan {
   int rows, nt, row_tiles, piece, n_pieces;
 };
@@ -1222,7 +1226,7 @@ constexpr int kMinPiece = cache4::kWarps;   // steps: one per warp
 AttendPlan attend_plan(int B, int H, int Hkv, int Nq, int max_len, int window_left) {
   AttendPlan a;
   a.rows = H / Hkv * Nq;
-  a.nt = a.rows <= 8 ? 1 : 2;
+  a.nt = a.rows <= 8 ? 1 : a.rows > 16 && a.rows <= 24 ? 3 : 2;
   a.row_tiles = (a.rows + 8 * a.nt - 1) / (8 * a.nt);
   long long span = std::max(max_len, 1);
   if (window_left >= 0)
@@ -1261,10 +1265,12 @@ template <Elt E, int kMods>
 fa_status launch_attend(int d, int nt, unsigned grid, cudaStream_t s, const cache4::AttendParams& p) {
   constexpr int T = cache4::kWarps * 32;
   if (d == 64)
-    return nt == 1 ? launch(cache4::attend_kernel<64, E, 1, kMods>, grid, T, 0, s, p)
-                   : launch(cache4::attend_kernel<64, E, 2, kMods>, grid, T, 0, s, p);
-  return nt == 1 ? launch(cache4::attend_kernel<128, E, 1, kMods>, grid, T, 0, s, p)
-                 : launch(cache4::attend_kernel<128, E, 2, kMods>, grid, T, 0, s, p);
+    return nt == 1   ? launch(cache4::attend_kernel<64, E, 1, kMods>, grid, T, 0, s, p)
+           : nt == 2 ? launch(cache4::attend_kernel<64, E, 2, kMods>, grid, T, 0, s, p)
+                     : launch(cache4::attend_kernel<64, E, 3, kMods>, grid, T, 0, s, p);
+  return nt == 1   ? launch(cache4::attend_kernel<128, E, 1, kMods>, grid, T, 0, s, p)
+         : nt == 2 ? launch(cache4::attend_kernel<128, E, 2, kMods>, grid, T, 0, s, p)
+                   : launch(cache4::attend_kernel<128, E, 3, kMods>, grid, T, 0, s, p);
 }
 
 template <Elt E>

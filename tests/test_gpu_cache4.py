@@ -116,6 +116,10 @@ CASES = [
     (2, 8, 1, 1, 64, HF, 64, [65, 500], dict(softcap=30.0)),
     (1, 14, 2, 1, 128, BF, 64, [777], dict(softcap=5.0, slopes=True)),
     (2, 16, 1, 1, 128, BF, 128, [300, 129], dict(slopes=True)),
+    (2, 17, 1, 1, 128, HF, 64, [70, 515], dict(softcap=8.0, slopes=True)),
+    (1, 24, 1, 1, 64, BF, 16, [1500], {}),
+    (3, 12, 2, 4, 64, HF, 32, [2, 33, 700], dict(window_left=64, slopes=True)),
+    (2, 25, 1, 1, 128, BF, 64, [64, 321], dict(softcap=8.0)),
     (2, 64, 2, 1, 64, BF, 256, [513, 40], {}),
     (2, 4, 4, 5, 128, BF, 32, [3, 200], {}),  # a draft longer than its sequence
     (2, 6, 2, 8, 64, HF, 16, [8, 333], dict(window_left=100)),
