@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int r = row0 + nt * 8 + g;
 #pragma unroll
     for (int w = 0; w < D / 32; ++w)
-      qw[nt][w] = r < p.rows ? *reinterpret_cast<const uint4*>(p.Q + out_row(r) * D + t * (D / 4) + 8 * w)
+      qw[nt][w] = r < p.rows ? *reinterpret_cast<const uint4*>(p.Q + out_row(r) * D +
+                                                               t * (D / 4) + 8 * w)
                              : make_uint4(0u, 0u, 0u, 0u);
   }
   int use = s_lo + piece * p.piece + warp, use_in = 0;
@@ -717,10 +718,14 @@ __global__ void __launch_bounds__(kWarps * 32)
         const uint32_t hi0 = __byte_perm(v[0][w], v[1][w], 0x7632);
         const uint32_t hi1 = __byte_perm(v[2][w], v[3][w], 0x7632);
         const uint32_t a[4][4] = {
-            {centred<Elt::BF16, 0>(lo0), centred<Elt::BF16, 1>(lo0), centred<Elt::BF16, 0>(lo1), centred<Elt::BF16, 1>(lo1)},
-            {centred<Elt::BF16, 2>(lo0), centred<Elt::BF16, 3>(lo0), centred<Elt::BF16, 2>(lo1), centred<Elt::BF16, 3>(lo1)},
-            {centred<Elt::BF16, 0>(hi0), centred<Elt::BF16, 1>(hi0), centred<Elt::BF16, 0>(hi1), centred<Elt::BF16, 1>(hi1)},
-            {centred<Elt::BF16, 2>(hi0), centred<Elt::BF16, 3>(hi0), centred<Elt::BF16, 2>(hi1), centred<Elt::BF16, 3>(hi1)}};
+            {centred<Elt::BF16, 0>(lo0), centred<Elt::BF16, 1>(lo0),
+             centred<Elt::BF16, 0>(lo1), centred<Elt::BF16, 1>(lo1)},
+            {centred<Elt::BF16, 2>(lo0), centred<Elt::BF16, 3>(lo0),
+             centred<Elt::BF16, 2>(lo1), centred<Elt::BF16, 3>(lo1)},
+            {centred<Elt::BF16, 0>(hi0), centred<Elt::BF16, 1>(hi0),
+             centred<Elt::BF16, 0>(hi1), centred<Elt::BF16, 1>(hi1)},
+            {centred<Elt::BF16, 2>(hi0), centred<Elt::BF16, 3>(hi0),
+             centred<Elt::BF16, 2>(hi1), centred<Elt::BF16, 3>(hi1)}};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -1219,8 +1219,8 @@ constexpr int kMinPiece = cache4::kWarps;   // steps: one per warp
 
 // Few heads are cut into many pieces of equal work, one wave of CTAs; more pieces cost more
 // to join and leave each warp fewer steps behind its start (kAttendCtas 296 / 444 / 592 / 1184:
-// B8 H16 Hkv4 five tokens over 2047 keys 20.9 / 17.9 / 20.4 / 21.2 us, B1 H32 Hkv4 L131071 37.8
-// us up to 592 and 45 us at 1184). Where there are many heads their sequences differ in length,
+// B8 H16 Hkv4 five tokens over 2047 keys, 16 rows a CTA, 20.9 / 17.9 / 20.4 / 21.2 us, B1 H32
+// Hkv4 L131071 37.8 us up to 592 and 45 us at 1184). Where there are many heads their sequences differ in length,
 // and finer pieces even that out (B64 H32 Hkv8, lengths 2048 to 8192: kAttendFine 1 / 2 / 4 / 6
 // / 8: 216 / 151 / 134 / 130 / 131 us).
 AttendPlan attend_plan(int B, int H, int Hkv, int Nq, int max_len, int window_left) {
@@ -1327,10 +1327,10 @@ fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* cod
   if (st != FA_OK || a.n_pieces == 1) return st;
   const unsigned blocks = static_cast<unsigned>(rows);
   if (d == 64)
-    return launch(cache4::combine_kernel<64, E>, blocks, cache4::kJoinThreads, 0, s, p.part_o, p.part_ml, p.O, LSE,
-                  a.n_pieces);
-  return launch(cache4::combine_kernel<128, E>, blocks, cache4::kJoinThreads, 0, s, p.part_o, p.part_ml, p.O, LSE,
-                a.n_pieces);
+    return launch(cache4::combine_kernel<64, E>, blocks, cache4::kJoinThreads, 0, s, p.part_o,
+                  p.part_ml, p.O, LSE, a.n_pieces);
+  return launch(cache4::combine_kernel<128, E>, blocks, cache4::kJoinThreads, 0, s, p.part_o,
+                p.part_ml, p.O, LSE, a.n_pieces);
 }
 
 }  // namespace
