@@ -16,6 +16,10 @@ Two forms:
     ``gather_heads`` assembles the full output on every rank when the caller wants
     it (an all-gather of outputs, outside the attention computation itself).
 
+K/V heads shared by groups of query heads: the flattened B*Hkv K/V heads are cut instead, and a
+shard takes the query heads that use its K/V heads, which are one contiguous range too (a rank
+of its own cuts ``rank_heads(B, Hkv, ...)`` and takes H / Hkv times that range of q).
+
 Dropout: the keep mask is keyed by the head index, so each shard passes its first
 flattened head as head_base (fa_forward_dropout_heads) and draws exactly the masks
 the unsharded call draws for its heads.
@@ -70,6 +74,22 @@ def _piece(t: torch.Tensor, a: int, b: int, dev: torch.device) -> torch.Tensor:
     return _flat(t)[a:b].to(dev, non_blocking=True).unsqueeze(0)
 
 
+def _shards(q, k, v, devs):
+    """[(query heads [a, b), K/V heads [ka, kb), device)] of the shards that hold heads: ranges of
+    the flattened K/V heads, and the query heads that share them. The whole call's shapes are
+    checked here, since a shard's alone may agree where the call's do not."""
+    B, H, N, d = q.shape
+    Hkv = k.shape[1] if k.dim() == 4 else 0
+    if k.shape != v.shape or k.shape != (B, Hkv, N, d):
+        raise ValueError(f"k and v must be [{B}, K/V heads, {N}, {d}] tensors, got "
+                         f"{tuple(k.shape)} and {tuple(v.shape)}")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError(f"{H} query heads cannot share {Hkv} K/V heads evenly")
+    group = H // Hkv
+    return [((ka * group, kb * group), (ka, kb), dev)
+            for (ka, kb), dev in zip(shard_ranges(B * Hkv, len(devs)), devs) if ka < kb]
+
+
 def _mask_on(block_mask, dev):
     return None if block_mask is None else block_mask.to(dev, non_blocking=True)
 
@@ -88,16 +108,14 @@ def forward_sharded(q, k, v, devices, causal: bool = False, scale=None, window=N
     CUDA devices; one may appear more than once). Inputs and outputs live on q's
     device; each shard's inputs are copied to its GPU and its outputs copied back.
     ``dropout`` = (p, seed, offset) as for api.forward draws the unsharded call's
-    masks."""
-    devs = _devices(devices)
-    B, H, N, d = q.shape
+    masks. k and v may have fewer heads than q, as for api.forward (without dropout and
+    block_mask)."""
+    shards = _shards(q, k, v, _devices(devices))
     o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    for (a, b), dev in zip(shard_ranges(B * H, len(devs)), devs):
-        if a == b:
-            continue
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    for (a, b), (ka, kb), dev in shards:
         with torch.cuda.device(dev):
-            qs, ks, vs = (_piece(t, a, b, dev) for t in (q, k, v))
+            qs, ks, vs = _piece(q, a, b, dev), _piece(k, ka, kb, dev), _piece(v, ka, kb, dev)
             os_, ls = api.forward(qs, ks, vs, causal, scale, window, _mask_on(block_mask, dev),
                                   _shard_dropout(dropout, a))
             _flat(o)[a:b].copy_(os_[0], non_blocking=True)
@@ -110,19 +128,17 @@ def backward_sharded(q, k, v, o, lse, do, devices, causal: bool = False, scale=N
     """(dQ, dK, dV) of the loss <dO, O>, computed in head shards on ``devices``, with
     the same masks and dropout as the forward. Each shard's backward workspace is
     allocated on its own GPU."""
-    devs = _devices(devices)
-    B, H, N, d = q.shape
+    shards = _shards(q, k, v, _devices(devices))
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    for (a, b), dev in zip(shard_ranges(B * H, len(devs)), devs):
-        if a == b:
-            continue
+    for (a, b), (ka, kb), dev in shards:
         with torch.cuda.device(dev):
-            qs, ks, vs, os_, dos = (_piece(t, a, b, dev) for t in (q, k, v, o, do))
-            ls = _piece(lse, a, b, dev)
+            qs, os_, dos, ls = (_piece(t, a, b, dev) for t in (q, o, do, lse))
+            ks, vs = (_piece(t, ka, kb, dev) for t in (k, v))
             g = api.backward(qs, ks, vs, os_, ls, dos, causal, scale, None, window,
                              _mask_on(block_mask, dev), _shard_dropout(dropout, a))
-            for dst, src in zip((dq, dk, dv), g):
-                _flat(dst)[a:b].copy_(src[0], non_blocking=True)
+            _flat(dq)[a:b].copy_(g[0][0], non_blocking=True)
+            for dst, src in zip((dk, dv), g[1:]):
+                _flat(dst)[ka:kb].copy_(src[0], non_blocking=True)
     return dq, dk, dv
 
 
