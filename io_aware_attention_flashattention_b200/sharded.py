@@ -70,8 +70,11 @@ def _devices(devices):
 
 
 def _piece(t: torch.Tensor, a: int, b: int, dev: torch.device) -> torch.Tensor:
-    """Heads [a, b) of a flattened tensor on ``dev`` as a [1, b - a, ...] tensor."""
-    return _flat(t)[a:b].to(dev, non_blocking=True).unsqueeze(0)
+    """Heads [a, b) of a flattened tensor on ``dev`` as a [1, b - a, ...] tensor. On t's own
+    device that is a view, and a head's LSE need not start on the 16 bytes that the library
+    asks for (N not a multiple of 4): it is copied then."""
+    x = _flat(t)[a:b].to(dev, non_blocking=True).unsqueeze(0)
+    return x.clone() if x.data_ptr() % 16 else x
 
 
 def _shards(q, k, v, devs):

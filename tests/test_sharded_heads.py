@@ -86,3 +86,21 @@ def test_shared_heads_match_the_unsharded_call(B, H, Hkv, N, d, dtype, causal, n
     out.backward(do)
     assert torch.equal(out, o)
     assert torch.equal(leaves[1].grad, grads[1]) and torch.equal(leaves[2].grad, grads[2])
+
+
+def test_a_piece_starts_on_16_bytes():
+    lse = torch.arange(5 * 77, dtype=torch.float32).reshape(1, 5, 77)
+    for a, b in sharded.shard_ranges(5, 3):
+        x = sharded._piece(lse, a, b, torch.device("cpu"))
+        assert x.data_ptr() % 16 == 0 and torch.equal(x[0], lse[0, a:b])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [77, 129, 1])
+def test_rows_of_any_length_on_the_tensors_own_device(N):
+    q, k, v, do = (torch.randn(1, 5, N, 64, device="cuda").to(BF) for _ in range(4))
+    o, lse = api.forward(q, k, v, True)
+    got = sharded.backward_sharded(q, k, v, o, lse, do, ["cuda:0"] * 3, True)
+    want = api.backward(q, k, v, o, lse, do, True)
+    torch.cuda.synchronize()
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
