@@ -429,7 +429,9 @@ __global__ void __launch_bounds__(kWarps * 32)
 
   // Copies of one group into part 2 * buffer + (0, 1) of the warp's ring: a thread's units of
   // the K and V codes (unit lane of each 512 bytes) and one of the 32 pairs. A group without
-  // a page takes page 0 instead (the reads stay inside the cache) and is marked.
+  // a page takes page 0 instead (the reads stay inside the cache) and is marked. So is a group in
+  // front of every row's window, which is not looked up (its page may be gone): the first half
+  // of step s_lo may be one, and no other step walked, so only the first call has a `from`.
   const uint32_t ring = smem_u32(smem) + warp * (4 * kPart);
   const unsigned page_groups = p.L.shift - 4;  // log2 of the groups per page
   const unsigned n_pages = static_cast<unsigned>(p.L.n_pages);
@@ -446,14 +448,16 @@ __global__ void __launch_bounds__(kWarps * 32)
     dst_k[u] = ring + ring_unit<D>(0, unit / kPerRow, unit % kPerRow) * 16;
     dst_v[u] = ring + kHalf + ring_unit<D>(1, unit / kPerRow, unit % kPerRow) * 16;
   }
-  unsigned bad = 0;  // parts whose group has no page
-  auto issue = [&](int x, int buffer) {  // the step x
+  unsigned bad = 0;  // bits of the parts whose group is not there; 4 up: because it lies in front
+  auto issue = [&](int x, int buffer, int from) {  // the step x, its groups from `from` on
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const int grp = 2 * x + part, slot = 2 * buffer + part;
-      if (grp < g_hi) {
+      if (grp < from) {
+        bad |= 0x11u << slot;
+      } else if (grp < g_hi) {
         unsigned id = static_cast<unsigned>(table[grp >> page_groups]);
-        bad &= ~(1u << slot);
+        bad &= ~(0x11u << slot);
         if (id >= n_pages) {
           bad |= 1u << slot;
           id = 0;
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   int use = s_lo + piece * p.piece + warp, use_in = 0;
   int ahead = use, ahead_in = 0;
-  issue(ahead, 0);
+  issue(ahead, 0, first / kGroup);
   ahead = next(ahead, ahead_in);
   uint32_t q[NT][KS][2];
   float qs[NT][2];
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int buffer = 0; use < s_hi; buffer ^= 1) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();  // every lane's copies are in, and every lane is done with the other buffer
-    issue(ahead, buffer ^ 1);
+    issue(ahead, buffer ^ 1, 0);
     ahead = next(ahead, ahead_in);
     const int step = use;
     use = next(use, use_in);
@@ -568,8 +572,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     for (int part = 0; part < 2; ++part) {
       const int k0 = (2 * step + part) * kGroup, slot = 2 * buffer + part;
       if (k0 >= len) break;
-      if ((bad >> slot) & 1u) {  // tokens without a page are not there
-        if (lane == 0) atomicOr(&g_status, kStatusBadPage);
+      if ((bad >> slot) & 1u) {  // not there; noted if for want of a page
+        if (lane == 0 && ((bad >> slot) & 0x10u) == 0u) atomicOr(&g_status, kStatusBadPage);
         continue;
       }
       const uint32_t off = slot * kPart;
