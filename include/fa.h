@@ -342,7 +342,8 @@ fa_status fa_score_span(const int32_t* documents, int n_docs, const int32_t* pre
  * bits and a pair (scale, zero) in the model's 16-bit type:
  *   zero = min x, scale = max x / 15 - min x / 15 rounded to the type,
  *   code = round((x - zero) / scale) to nearest even, within 0..15 (0 where scale is 0),
- *   value = scale * code + zero.
+ *   value = scale * code + zero (an infinity where the rounded scale takes it past the type's
+ *   largest number, which max x is then within a sixteenth of a step of).
  *   codes:  DEVICE bytes [n_pages, 2, Hkv, page, d / 2] (index 0 of the second axis K, 1 V);
  *           channel 2c is the low half of byte c, channel 2c + 1 the high half.
  *   params: DEVICE [n_pages, 2, Hkv, page, 2] of the model's type, (scale, zero).

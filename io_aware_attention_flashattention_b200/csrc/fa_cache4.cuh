@@ -139,8 +139,9 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
 // 16-bit values, so a test for them sent most warps to a division each. Adding 1.5 * 2^23
 // rounds and leaves the code in the low bits; the sum of the shifted bits holds a constant
 // beside the codes. Where the scale is below the type's normal numbers (codes may pass 15, and
-// the products may leave the normal range) or x - lo passes 32 bits the quotients are formed
-// one by one.
+// the products may leave the normal range) or x - lo may pass 32 bits the quotients are formed
+// one by one, of halves: 0.5 x - 0.5 lo stays in range, and halving is exact (16-bit values
+// and their differences are multiples of 2^-133, 32 bits hold those of 2^-149).
 template <Elt E>
 __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], float lo, float hi, float scale) {
   constexpr float kMagic = 12582912.0f;
@@ -169,8 +170,8 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], float lo, floa
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const float2 x = unpack2<E>(w[k / 2]);
-      const float c =
-          fminf(fmaxf(rintf(__fdiv_rn(((k & 1) ? x.y : x.x) - lo, scale)), 0.0f), 15.0f);
+      const float d = __fsub_rn(0.5f * ((k & 1) ? x.y : x.x), 0.5f * lo);
+      const float c = fminf(fmaxf(rintf(__fdiv_rn(d, 0.5f * scale)), 0.0f), 15.0f);
       code[k / 8] |= static_cast<uint32_t>(c) << (4 * (k % 8));
     }
   }
