@@ -11,6 +11,8 @@
 // table[b][t / page]. Pages hold whole groups of 16 tokens, so no group straddles two.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_ptx.cuh"
 #include "fa_score.cuh"
 
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   // the K and V codes (unit lane of each 512 bytes) and one of the 32 pairs. A group without
   // a page takes page 0 instead (the reads stay inside the cache) and is marked. So is a group in
   // front of every row's window, which is not looked up (its page may be gone): the first half
-  // of step s_lo may be one, and no other step walked, so only the first call has a `from`.
+  // of step s_lo may be one, and no other, so only the first call looks for it.
   const uint32_t ring = smem_u32(smem) + warp * (4 * kPart);
   const unsigned page_groups = p.L.shift - 4;  // log2 of the groups per page
   const unsigned n_pages = static_cast<unsigned>(p.L.n_pages);
@@ -450,11 +452,12 @@ __global__ void __launch_bounds__(kWarps * 32)
     dst_v[u] = ring + kHalf + ring_unit<D>(1, unit / kPerRow, unit % kPerRow) * 16;
   }
   unsigned bad = 0;  // bits of the parts whose group is not there; 4 up: because it lies in front
-  auto issue = [&](int x, int buffer, int from) {  // the step x, its groups from `from` on
+  // the step x; kFirst: its groups in front of `first` are marked
+  auto issue = [&](int x, int buffer, auto kFirst) {
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const int grp = 2 * x + part, slot = 2 * buffer + part;
-      if (grp < from) {
+      if (decltype(kFirst)::value && grp < first / kGroup) {
         bad |= 0x11u << slot;
       } else if (grp < g_hi) {
         unsigned id = static_cast<unsigned>(table[grp >> page_groups]);
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   int use = s_lo + piece * p.piece + warp, use_in = 0;
   int ahead = use, ahead_in = 0;
-  issue(ahead, 0, first / kGroup);
+  issue(ahead, 0, std::true_type{});
   ahead = next(ahead, ahead_in);
   uint32_t q[NT][KS][2];
   float qs[NT][2];
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int buffer = 0; use < s_hi; buffer ^= 1) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();  // every lane's copies are in, and every lane is done with the other buffer
-    issue(ahead, buffer ^ 1, 0);
+    issue(ahead, buffer ^ 1, std::false_type{});
     ahead = next(ahead, ahead_in);
     const int step = use;
     use = next(use, use_in);
