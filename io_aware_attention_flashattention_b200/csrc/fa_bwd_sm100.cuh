@@ -560,7 +560,7 @@ __device__ __forceinline__ void p_ds_quarter(uint32_t tm_s, uint32_t tm_dp, cons
     // tanh of the chunk's scores, kept apart from the bias for the derivative
     [[maybe_unused]] uint32_t th[(kScore & kScoreCap) ? 16 : 1];
     if constexpr ((kScore & kScoreCap) != 0) {
-      tanh_scores<16>(sv, score);
+      tanh_scores<16, (kScore & kScoreFar) != 0>(sv, score);
 #pragma unroll
       for (int k = 0; k < 16; ++k) th[k] = sv[k];
     }

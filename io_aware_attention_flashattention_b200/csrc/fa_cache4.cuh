@@ -368,7 +368,7 @@ __host__ __device__ constexpr int ring_unit(int which, int row, int unit) {
                     : (D == 128 ? at ^ (((row >> 1) & 1) << 1) : at);
 }
 
-// kMods: kScoreCap and kScoreBias.
+// kMods: kScoreCap, kScoreBias and kScoreFar.
 template <int D, Elt E, int NT, int kMods>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_kernel(const AttendParams p) {
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kWarps * 32)
           u[4 * nt + e] =
               __float_as_uint(fmaf(ksz[e >> 1].x, s[nt][e], ksz[e >> 1].y * qs[nt][e & 1]));
       if constexpr ((kMods & kScoreCap) != 0) {
-        tanh_scores<4 * NT>(u, p.score);
+        tanh_scores<4 * NT, (kMods & kScoreFar) != 0>(u, p.score);
 #pragma unroll
         for (int e = 0; e < 4 * NT; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * c);
       }

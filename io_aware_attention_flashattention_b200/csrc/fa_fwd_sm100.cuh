@@ -410,7 +410,7 @@ __device__ __forceinline__ bool scored_half_tile(const Params& p, const Watchdog
   if constexpr (kCap) {
     if (!fused) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tanh_scores<16>(&s[q / 2][(q & 1) * 16], p.score);
+      for (int q = 0; q < 4; ++q) tanh_scores<16, (kScore & kScoreFar) != 0>(&s[q / 2][(q & 1) * 16], p.score);
     }
   }
   float base = 0.0f, sl = 0.0f;

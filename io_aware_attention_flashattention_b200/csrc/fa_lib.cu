@@ -176,6 +176,8 @@ cudaError_t set_smem_d() {
   e = e ? e : set_smem_score<D, E, kScoreOn | kScoreCap>();
   e = e ? e : set_smem_score<D, E, kScoreOn | kScoreBias>();
   e = e ? e : set_smem_score<D, E, kScoreOn | kScoreCap | kScoreBias>();
+  e = e ? e : set_smem_score<D, E, kScoreOn | kScoreCap | kScoreFar>();
+  e = e ? e : set_smem_score<D, E, kScoreOn | kScoreCap | kScoreBias | kScoreFar>();
   return e;
 }
 
@@ -894,8 +896,7 @@ fa_status backward_impl(const void* Q, const void* K, const void* V, const void*
 // softcap 0: none. The polynomial of tanh (see kTanhQ5) takes the powers of a = scale / cap
 // into its coefficients, up to a^9, which must stay normal numbers: for a >= 2^-13 it is used
 // up to |x| = 0.8; below, its Taylor form of three terms up to |x| = 0.05, where the next
-// term is 8e-10 of the result. 1 - 2 / (1 + e^2x) takes over above, where its absolute
-// error of 6.3e-7 is small next to x. So a is held to [2^-24, 2^12].
+// term is 8e-10 of the result. Above, tanh_scores says what takes over. a is held to [2^-24, 2^12].
 fa_status make_score(int B, int H, int Hkv, float scale, float softcap, const float* slopes,
                      const int32_t* documents, int n_docs, const int32_t* prefix,
                      ScoreParams* s) {
@@ -928,6 +929,7 @@ fa_status make_score(int B, int H, int Hkv, float scale, float softcap, const fl
     }
     const double lim5 = (full ? kTanhLimit5 : 0.05) / a;
     s->lim5 = static_cast<float>(lim5 * lim5);
+    s->cap_in = static_cast<float>(a);
     s->cap_in2 = static_cast<float>(2.0 * 1.4426950408889634 * a);
   }
   s->slope_mul = softcap > 0.0f ? 1.0f / softcap : 1.0f / scale;
@@ -936,7 +938,8 @@ fa_status make_score(int B, int H, int Hkv, float scale, float softcap, const fl
 }
 
 int score_bits(float softcap, const float* slopes) {
-  return kScoreOn | (softcap > 0.0f ? kScoreCap : 0) | (slopes != nullptr ? kScoreBias : 0);
+  return kScoreOn | (softcap > 0.0f ? kScoreCap : 0) | (softcap > kNearCap ? kScoreFar : 0) |
+         (slopes != nullptr ? kScoreBias : 0);
 }
 
 // Scores before this factor to log2 units (see fa_score.cuh).
@@ -996,12 +999,14 @@ fa_status forward_scored_impl(const void* Q, const void* K, const void* V, void*
   p.timeout_ns = watchdog_ns();
   const unsigned grid = static_cast<unsigned>(p.n_items);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  constexpr int On = kScoreOn, Cap = kScoreCap, Bias = kScoreBias;
+  constexpr int On = kScoreOn, Cap = kScoreCap, Bias = kScoreBias, Far = kScoreFar;
   switch (score_bits(softcap, slopes)) {
     case On: return launch_fwd_scored<E, On>(d, grid, s, mq, mk, mv, p);
     case On | Cap: return launch_fwd_scored<E, On | Cap>(d, grid, s, mq, mk, mv, p);
     case On | Bias: return launch_fwd_scored<E, On | Bias>(d, grid, s, mq, mk, mv, p);
-    default: return launch_fwd_scored<E, On | Cap | Bias>(d, grid, s, mq, mk, mv, p);
+    case On | Cap | Bias: return launch_fwd_scored<E, On | Cap | Bias>(d, grid, s, mq, mk, mv, p);
+    case On | Cap | Far: return launch_fwd_scored<E, On | Cap | Far>(d, grid, s, mq, mk, mv, p);
+    default: return launch_fwd_scored<E, On | Cap | Bias | Far>(d, grid, s, mq, mk, mv, p);
   }
 }
 
@@ -1123,12 +1128,18 @@ fa_status backward_scored_impl(const void* Q, const void* K, const void* V, cons
                      ? 1
                      : 0;
   const unsigned grid = static_cast<unsigned>(n_tiles * p.n_seg);
-  constexpr int On = kScoreOn, Cap = kScoreCap, Bias = kScoreBias;
+  constexpr int On = kScoreOn, Cap = kScoreCap, Bias = kScoreBias, Far = kScoreFar;
   switch (score_bits(softcap, slopes)) {
     case On: st = launch_bwd_scored<E, On>(d, grid, s, mq, mk, mv, mdo, p); break;
     case On | Cap: st = launch_bwd_scored<E, On | Cap>(d, grid, s, mq, mk, mv, mdo, p); break;
     case On | Bias: st = launch_bwd_scored<E, On | Bias>(d, grid, s, mq, mk, mv, mdo, p); break;
-    default: st = launch_bwd_scored<E, On | Cap | Bias>(d, grid, s, mq, mk, mv, mdo, p);
+    case On | Cap | Bias:
+      st = launch_bwd_scored<E, On | Cap | Bias>(d, grid, s, mq, mk, mv, mdo, p);
+      break;
+    case On | Cap | Far:
+      st = launch_bwd_scored<E, On | Cap | Far>(d, grid, s, mq, mk, mv, mdo, p);
+      break;
+    default: st = launch_bwd_scored<E, On | Cap | Bias | Far>(d, grid, s, mq, mk, mv, mdo, p);
   }
   if (st != FA_OK) return st;
   return dq_convert_impl<E>(dQ, B, H, N, d, scale, workspace, workspace_bytes, stream, false);
@@ -1322,7 +1333,9 @@ fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* cod
     case 0: st = launch_attend<E, 0>(d, a.nt, grid, s, p); break;
     case kScoreCap: st = launch_attend<E, kScoreCap>(d, a.nt, grid, s, p); break;
     case kScoreBias: st = launch_attend<E, kScoreBias>(d, a.nt, grid, s, p); break;
-    default: st = launch_attend<E, kScoreCap | kScoreBias>(d, a.nt, grid, s, p);
+    case kScoreCap | kScoreBias: st = launch_attend<E, kScoreCap | kScoreBias>(d, a.nt, grid, s, p); break;
+    case kScoreCap | kScoreFar: st = launch_attend<E, kScoreCap | kScoreFar>(d, a.nt, grid, s, p); break;
+    default: st = launch_attend<E, kScoreCap | kScoreBias | kScoreFar>(d, a.nt, grid, s, p);
   }
   if (st != FA_OK || a.n_pieces == 1) return st;
   const unsigned blocks = static_cast<unsigned>(rows);

@@ -19,6 +19,7 @@ namespace fa {
 constexpr int kScoreOn = 1;    // documents, prefix, shared K/V heads
 constexpr int kScoreCap = 2;   // tanh cap
 constexpr int kScoreBias = 4;  // distance bias
+constexpr int kScoreFar = 8;   // with kScoreCap: a cap above kNearCap (see tanh_scores)
 
 struct ScoreParams {
   const float* slopes;  // [H], or null
@@ -32,6 +33,7 @@ struct ScoreParams {
   // units), and the bound on s^2 up to which it holds (see make_score)
   float q5[5], cq5[5];
   float lim5;
+  float cap_in;       // scale / cap
   float cap_in2;      // 2 * log2(e) * scale / cap, for the form on the exponential; 0: no cap
   float slope_mul;    // a slope times this is in units of the scores before c (below)
 };
@@ -41,6 +43,10 @@ struct ScoreParams {
 constexpr double kTanhLimit5 = 0.8;
 constexpr double kTanhQ5[5] = {0.9999989944, -0.3332537202, 0.1323056571, -0.04918014249,
                                0.01210013727};
+
+// The form of tanh on the exponential is off by up to 6.3e-7, times the cap: up to this cap by 4e-5
+// of a score, a twelfth of a rounding of its weight to f16.
+constexpr float kNearCap = 64.0f;
 
 struct Span {
   int lo, hi;
@@ -211,9 +217,9 @@ __device__ __forceinline__ void share_documents(int* shared, int room, int n_doc
   if (prefix) prefix = shared + n_docs + 1;
 }
 
-// tanh of one score of any size: 1 - 2 / (1 + e^2x), by the exponential and the reciprocal
-// of the MUFU unit. Absolute error up to 6.3e-7, which the cap multiplies: fit for |x| of the
-// order of one and more, where the polynomials do not reach.
+// tanh of one score: 1 - 2 / (1 + e^2x), by the exponential and the reciprocal of the MUFU
+// unit. Absolute error up to 6.3e-7, which the cap multiplies: fit where the polynomial does not
+// reach, |x| > 0.8 (9.5e-7 of the result there at most).
 __device__ __forceinline__ float tanh_exp(float s, float cap_in2) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(s * cap_in2)));
@@ -221,9 +227,13 @@ __device__ __forceinline__ float tanh_exp(float s, float cap_in2) {
 }
 
 // tanh in place of n scores held by this thread (n even). Which form is a warp's choice
-// (the branch would diverge otherwise): the polynomial where every score of the warp's
-// piece lies within its reach. Capped models keep most scores well inside the cap.
-template <int n>
+// (the branch would diverge otherwise): the polynomial where every score of the warp's piece
+// lies within its reach (capped models keep most well inside the cap), else the one on the
+// exponential. That form's error is absolute, and would show in scores near 0 of other rows
+// under a large cap; so above kNearCap (kFar) each score of such a piece takes the one or the
+// other by its own size, relative error 1.05e-6 either way. Taken at all caps it spilled
+// registers and cost every capped forward (B1 H8 N16384 d128 causal, cap 50: 711 -> 785 us).
+template <int n, bool kFar>
 __device__ __forceinline__ void tanh_scores(uint32_t* s, const ScoreParams& p) {
   float2 S[n / 2];
   float top = 0.0f;
@@ -234,9 +244,25 @@ __device__ __forceinline__ void tanh_scores(uint32_t* s, const ScoreParams& p) {
     top = fmax3(top, S[k].x, S[k].y);
   }
   if (__any_sync(0xffffffffu, !(top <= p.lim5))) {
+    if constexpr (kFar) {
+      constexpr float q[5] = {static_cast<float>(kTanhQ5[0]), static_cast<float>(kTanhQ5[1]),
+                              static_cast<float>(kTanhQ5[2]), static_cast<float>(kTanhQ5[3]),
+                              static_cast<float>(kTanhQ5[4])};
+      constexpr float kReach = static_cast<float>(kTanhLimit5 * kTanhLimit5);
 #pragma unroll
-    for (int k = 0; k < n; ++k)
-      s[k] = __float_as_uint(tanh_exp(__uint_as_float(s[k]), p.cap_in2));
+      for (int k = 0; k < n / 2; ++k) {
+        const float2 raw = make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+        const float2 x = fmul2(raw, make_float2(p.cap_in, p.cap_in)), X = fmul2(x, x);
+        const float2 r = fmul2(x, odd_poly2(X, q));
+        const float fx = tanh_exp(raw.x, p.cap_in2), fy = tanh_exp(raw.y, p.cap_in2);
+        s[2 * k] = __float_as_uint(X.x <= kReach ? r.x : fx);
+        s[2 * k + 1] = __float_as_uint(X.y <= kReach ? r.y : fy);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < n; ++k)
+        s[k] = __float_as_uint(tanh_exp(__uint_as_float(s[k]), p.cap_in2));
+    }
   } else {
 #pragma unroll
     for (int k = 0; k < n / 2; ++k) {
