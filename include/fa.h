@@ -108,7 +108,9 @@ size_t fa_backward_workspace_size(int B, int H, int N, int d);
  *                    16-byte aligned; its contents on entry do not matter and are
  *                    undefined on return.
  * dQ is accumulated in fp32 with atomic adds, so its last bits may differ from
- * run to run; dK and dV are deterministic.
+ * run to run; dK and dV are deterministic. Where the mask leaves every row its own key
+ * alone (N = 1, or a window of no neighbours on either side; dropout and block masks
+ * aside) dQ and dK are 0, exactly.
  */
 fa_status fa_backward(const void* Q, const void* K, const void* V, const void* O,
                       const void* dO, const float* LSE, void* dQ, void* dK, void* dV,

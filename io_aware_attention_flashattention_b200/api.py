@@ -669,9 +669,6 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale=None, workspace=No
     scale = _default_scale(d, scale)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     scored = _scored(q, k, window, block_mask, dropout, softcap, slopes, documents, prefix)
-    if (N == 1 and block_mask is None and dropout is None
-            and q.dtype in (torch.bfloat16, torch.float16)):
-        scored = True  # one token: dQ and dK are 0, which the scored backward gives exactly
     if workspace is not None:
         ws = workspace
     elif scored:

@@ -872,6 +872,23 @@ fa_status dq_convert_impl(void* dQ, int B, int H, int N, int d, float scale, voi
 }
 
 template <Elt E>
+fa_status backward_scored_impl(const void* Q, const void* K, const void* V, const void* O,
+                               const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                               int B, int H, int Hkv, int N, int d, float scale, int causal,
+                               int window_left, int window_right, float softcap,
+                               const float* slopes, const int32_t* documents, int n_docs,
+                               const int32_t* prefix, void* workspace, size_t workspace_bytes,
+                               fa_stream_t stream);
+
+// Does every row see its own key alone? Its weight is 1 whatever the scores, so dQ = dK = 0; the
+// plain kernels leave the rounding of dP - D there (dP and D are summed in different orders),
+// the scored ones give zeros. Masks that leave only some rows one key stay with the plain
+// kernels, whose loop a test for such rows would lengthen.
+bool one_key_rows(int N, const MaskSpec& mask, const DropSpec& drop) {
+  return !drop.on && mask.blocks == nullptr && (N == 1 || (mask.wl == 0 && mask.wr == 0));
+}
+
+template <Elt E>
 fa_status backward_impl(const void* Q, const void* K, const void* V, const void* O, const void* dO,
                       const float* LSE, void* dQ, void* dK, void* dV, int B, int H, int N, int d,
                       float scale, int causal, const MaskSpec& mask, const DropSpec& drop,
@@ -882,6 +899,10 @@ fa_status backward_impl(const void* Q, const void* K, const void* V, const void*
   fa_status st = bwd_plan(ptrs, 9, B, H, N, d, scale, causal, workspace, workspace_bytes, &pl,
                           split_ok);
   if (st != FA_OK || N == 0) return st;
+  if (one_key_rows(N, mask, drop))
+    return backward_scored_impl<E>(Q, K, V, O, dO, LSE, dQ, dK, dV, B, H, H, N, d, scale, causal,
+                                   mask.wl, mask.wr, 0.0f, nullptr, nullptr, 1, nullptr, workspace,
+                                   workspace_bytes, stream);
   st = preprocess_impl<E>(O, dO, LSE, B, H, N, d, scale, causal, workspace, workspace_bytes, stream,
                           split_ok);
   if (st != FA_OK) return st;
