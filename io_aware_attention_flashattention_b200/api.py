@@ -29,8 +29,9 @@ __all__ = [
     "fa_backward_noalloc", "fa_forward_f16", "fa_backward_f16", "fa_forward_masked",
     "fa_backward_masked", "fa_forward_dropout", "fa_backward_dropout", "fa_forward_f32",
     "fa_backward_f32", "fa_forward_scored", "fa_backward_scored", "fa_forward_scored_f16",
-    "fa_backward_scored_f16", "fa_cache4_append", "fa_cache4_read", "fa_cache4_attend",
-    "fa_cache4_append_f16", "fa_cache4_read_f16", "fa_cache4_attend_f16",
+    "fa_backward_scored_f16", "fa_backward_scored_workspace_size", "fa_cache4_append",
+    "fa_cache4_read", "fa_cache4_attend", "fa_cache4_append_f16", "fa_cache4_read_f16",
+    "fa_cache4_attend_f16", "fa_cache4_workspace_size",
     "fa_get_status", "fa_watchdog_selftest", "fa_version", "fa_dropout_rate",
     "fa_launch_plan",
     "forward", "backward", "attention", "FlashAttentionFunction", "cache4_empty",
