@@ -703,14 +703,15 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale=None, workspace=No
     return dq, dk, dv
 
 
+_SLOPES_CONSTANT = "slopes are constants: they have no gradient"
+
+
 class FlashAttentionFunction(torch.autograd.Function):
     """Differentiable exact attention through the library's forward and backward."""
 
     @staticmethod
     def forward(ctx, q, k, v, causal: bool = False, scale=None, window=None, block_mask=None,
                 dropout=None, softcap=None, slopes=None, documents=None, prefix=None):
-        if slopes is not None and slopes.requires_grad:
-            raise ValueError("slopes are constants: they have no gradient")
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         o, lse = forward(q, k, v, causal, scale, window, block_mask, dropout, softcap, slopes,
                          documents, prefix)
@@ -722,6 +723,8 @@ class FlashAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, do):
+        if ctx.needs_input_grad[9]:
+            raise ValueError(_SLOPES_CONSTANT)
         q, k, v, o, lse, slopes, documents, prefix = ctx.saved_tensors
         dq, dk, dv = backward(q, k, v, o, lse, do.contiguous(), ctx.causal, ctx.scale,
                               window=ctx.window, block_mask=ctx.block_mask,
@@ -734,11 +737,14 @@ def attention(q, k, v, causal: bool = False, scale=None, window=None, block_mask
               dropout=None, softcap=None, slopes=None, documents=None, prefix=None):
     """Differentiable attention; ``dropout`` = (p, seed, offset): pass a new offset (or
     seed) per call to draw a new mask. ``softcap``, ``slopes``, ``documents`` and
-    ``prefix`` as for ``forward``; slopes are constants (no gradient).
+    ``prefix`` as for ``forward``; slopes are constants, and those that require a gradient are
+    refused unless autograd is off.
 
     A backward pass may be captured into a CUDA graph, but not while an eager graph of the same
     leaves is alive (drop its outputs first): autograd would tie the captured pass to the
     eager one's stream, which ends the process."""
+    if slopes is not None and slopes.requires_grad and torch.is_grad_enabled():
+        raise ValueError(_SLOPES_CONSTANT)
     return FlashAttentionFunction.apply(q, k, v, causal, scale, window, block_mask, dropout,
                                         softcap, slopes, documents, prefix)
 
