@@ -352,8 +352,10 @@ __device__ __forceinline__ bool softmax_key_tile(const Params& p, const Watchdog
 // one that favoured scores far inside the cap), this way 0.75 / 0.84 / 1.11 ms; bias 0.69 ->
 // 0.64 ms, documents alone 0.49 ms either way (plain causal 0.47 ms). The two threads of a row
 // trade their maxima through TMEM: each writes its own to the first of its 64 columns of
-// S_t, which it has read by then. What bounds it now: issue (2.1 instructions per cycle with
-// a cap; the tensor pipe is 36% active).
+// S_t, which it has read by then. What bounds it now: the length of each tile's chain (S, the
+// traded maxima, exponents, P), neither issue nor the tensor pipe: 44% of the issue slots and 25% of
+// the tensor pipe at B2 H16 Hkv8 N8192 d128, window 1024, cap 30, the warps waiting on TMEM loads
+// and barriers.
 //
 // One key tile: what softmax_key_tile does, for columns [64 half, 64 half + 64).
 //   cap: tanh ascends, so the maximum may be taken of the raw scores, and the polynomial of

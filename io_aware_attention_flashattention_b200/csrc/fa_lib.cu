@@ -1245,16 +1245,24 @@ struct AttendPlan {
   int rows, nt, row_tiles, piece, n_pieces;
 };
 
+// CTAs to aim for. The workspace is sized by this plan, on a host that may have no GPU, so it counts
+// B200's 148 SMs rather than the current device's; three CTAs an SM, what the 16-row instance fits
+// at d = 128 (the 8-row one fits four, six at d = 64; the 24-row one two, so that its calls take
+// more than a wave).
 constexpr long long kAttendCtas = 148 * 3;
 constexpr long long kAttendFine = 6;
 constexpr int kMinPiece = cache4::kWarps;   // steps: one per warp
 
 // Few heads are cut into many pieces of equal work, one wave of CTAs; more pieces cost more
-// to join and leave each warp fewer steps behind its start (kAttendCtas 296 / 444 / 592 / 1184:
-// B8 H16 Hkv4 five tokens over 2047 keys, 16 rows a CTA, 20.9 / 17.9 / 20.4 / 21.2 us, B1 H32
-// Hkv4 L131071 37.8 us up to 592 and 45 us at 1184). Where there are many heads their sequences differ in length,
-// and finer pieces even that out (B64 H32 Hkv8, lengths 2048 to 8192: kAttendFine 1 / 2 / 4 / 6
-// / 8: 216 / 151 / 134 / 130 / 131 us).
+// to join and leave each warp fewer steps behind its start. In a graph, kAttendCtas 296 / 444 /
+// 592 / 1184: B8 H16 Hkv4 five tokens, window 2047, 14.2 / 14.2 / 18.7 / 18.6 us; the same heads,
+// four tokens over 2047 keys, 13.9 / 13.9 / 14.3 / 14.4; B1 H32 Hkv4 L131071 29.8 / 29.8 / 28.9 /
+// 31.2. Where there are many heads their sequences differ in length, and finer pieces even that
+// out (B64 H32 Hkv8, lengths 2048 to 8192: kAttendFine 1 / 2 / 4 / 6 / 8: 174 / 155 / 132 / 129 /
+// 128 us). The border between the two, 111 heads, is no optimum: at 104 heads of such lengths the
+// finer cut takes 35 us for 44 (d = 64: 25 for 42), at 120 heads 41 for 53 (27 for 50), but with
+// five tokens a sequence (24 rows a CTA) 52 for 48; a cut twice as fine as the coarse one lies
+// between or below both (32, 41, 44).
 AttendPlan attend_plan(int B, int H, int Hkv, int Nq, int max_len, int window_left) {
   AttendPlan a;
   a.rows = H / Hkv * Nq;
@@ -1338,7 +1346,6 @@ fa_status cache4_attend_impl(const void* Q, void* O, float* LSE, const void* cod
   p.part_ml = reinterpret_cast<float2*>(
       static_cast<char*>(workspace) +
       (a.n_pieces > 1 ? round256(static_cast<size_t>(rows) * a.n_pieces * d * sizeof(float)) : 0));
-  p.B = B;
   p.H = H;
   p.Nq = Nq;
   p.rows = a.rows;
